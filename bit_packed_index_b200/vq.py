@@ -1,4 +1,5 @@
-"""Python binding of libvq (include/vq.h): argument marshalling only.
+"""Python binding of libvq (include/vq.h, vq_i8.h, vq_experts.h): argument
+marshalling only.
 
 Every computation runs in the CUDA kernels behind the C ABI; this module only
 turns torch tensors into pointers, sizes and the current CUDA stream.  There
@@ -9,6 +10,12 @@ Names follow the C ABI: ``dequant``, ``gemv``, ``gemv_multi``, ``gemv_rht``,
 workspace size queries.  A ``Layer`` holds the device tensors of one
 quantised layer (packed index streams in row order or in the tiled order,
 fp16 codebooks, optional fp16 scale and bias, optional fp16 output bias).
+
+Beside them stand layers in 8-bit integers (``Int8Layer``, ``quant_i8``,
+``gemm_i8``, ``linear_i8``) and the experts of a mixture (``Experts``,
+``group_rows``, ``gemm_experts``, ``combine_rows``).  Those calls check their
+tensors' types, shapes, strides and device and raise ``ValueError``, and run on
+their tensors' device whatever the current one is.
 """
 from __future__ import annotations
 
@@ -24,6 +31,8 @@ import torch
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libvq.so")
 HEADER = os.path.join(os.path.dirname(HERE), "include", "vq.h")
+HEADER_I8 = os.path.join(os.path.dirname(HERE), "include", "vq_i8.h")
+HEADER_EXPERTS = os.path.join(os.path.dirname(HERE), "include", "vq_experts.h")
 
 VQ_OK, VQ_ERR_INVALID_ARG, VQ_ERR_UNSUPPORTED, VQ_ERR_ALIGNMENT = 0, 1, 2, 3
 VQ_ERR_WORKSPACE, VQ_ERR_CUDA, VQ_ERR_TIMEOUT = 4, 5, 6
@@ -63,13 +72,28 @@ class _EncDesc(C.Structure):
     ]
 
 
+class _I8Desc(C.Structure):
+    _fields_ = [
+        ("out_features", C.c_int32), ("in_features", C.c_int32),
+        ("w", C.c_void_p), ("ldw", C.c_int64), ("scale", C.c_void_p), ("out_bias", C.c_void_p),
+    ]
+
+
+class _ExpertsDesc(C.Structure):
+    _fields_ = [
+        ("layer", _Desc), ("n_experts", C.c_int32), ("reserved", C.c_int32),
+        ("idx_stride", C.c_int64 * 2), ("codebook_stride", C.c_int64 * 2),
+        ("scale_stride", C.c_int64), ("bias_stride", C.c_int64), ("out_bias_stride", C.c_int64),
+    ]
+
+
 _lock = threading.Lock()
 _lib = None
 
 
-def exported_names() -> List[str]:
-    """Function names the header declares (VQ_API ...)."""
-    with open(HEADER) as fh:
+def exported_names(header: str = HEADER) -> List[str]:
+    """Function names a header declares (VQ_API ...)."""
+    with open(header) as fh:
         text = fh.read()
     return re.findall(r"VQ_API\s+[\w\s\*]+?\b(vq_\w+)\s*\(", text)
 
@@ -100,6 +124,19 @@ def lib():
             L.vq_hessian.argtypes = [P, C.c_int, I32, I32, I64, P, I64, P, SZ, P]
             L.vq_encode_workspace_size.argtypes = [P, C.POINTER(SZ)]
             L.vq_encode.argtypes = [P, P, SZ, P]
+            L.vq_quant_i8.argtypes = [P, C.c_int, I32, I32, I64, P, I64, P, P]
+            L.vq_gemm_i8_workspace_size.argtypes = [P, I32, C.POINTER(SZ)]
+            L.vq_gemm_i8.argtypes = [P, P, I64, P, I32, P, C.c_int, I64, P, SZ, P]
+            L.vq_linear_i8_workspace_size.argtypes = [P, I32, C.POINTER(SZ)]
+            L.vq_linear_i8.argtypes = [P, P, C.c_int, I32, I64, P, C.c_int, I64, P, SZ, P]
+            L.vq_group_rows.argtypes = [P, I32, I32, I64, I32, P, P, P, P]
+            L.vq_gemm_experts_workspace_size.argtypes = [P, I32, C.POINTER(SZ)]
+            L.vq_gemm_experts.argtypes = [P, P, C.c_int, I32, I64, P, P, I32, P, C.c_int, I64, P, SZ, P]
+            L.vq_combine_rows.argtypes = [P, C.c_int, I32, I32, I64, P, P, I64, I32, I32, P, C.c_int, I64, P]
+            for fn in ("vq_quant_i8", "vq_gemm_i8_workspace_size", "vq_gemm_i8",
+                       "vq_linear_i8_workspace_size", "vq_linear_i8", "vq_group_rows",
+                       "vq_gemm_experts_workspace_size", "vq_gemm_experts", "vq_combine_rows"):
+                getattr(L, fn).restype = C.c_int
             for fn in ("vq_dequant", "vq_gemv_workspace_size", "vq_gemv", "vq_gemv_noalloc",
                        "vq_gemm_workspace_size", "vq_gemm", "vq_repack_tile4",
                        "vq_encode_workspace_size", "vq_encode", "vq_gemv_multi_workspace_size",
@@ -481,6 +518,342 @@ def encode(w: torch.Tensor, codebooks: Sequence[torch.Tensor], log2k: Sequence[i
     ws, ws_bytes = _workspace(n.value, w.device, workspace)
     _check("vq_encode", lib().vq_encode(C.byref(d), _ptr(ws), ws_bytes, C.c_void_p(_stream(w.device))))
     return Layer(w.shape[0], w.shape[1], vec_dim, log2k, idx, books)
+
+
+# ---------------------------------------------------------------------------
+# Layers in 8-bit integers (include/vq_i8.h).
+# ---------------------------------------------------------------------------
+_IN16 = (torch.bfloat16, torch.float16)
+
+
+def _need(ok: bool, what: str):
+    if not ok:
+        raise ValueError(what)
+
+
+def _matrix(t: torch.Tensor, name: str, dtypes, device) -> int:
+    """Row stride of a row-major matrix on `device`."""
+    _need(t.dim() == 2 and t.dtype in dtypes, f"{name} must be a matrix of {' or '.join(map(str, dtypes))}")
+    _need(t.device == device and t.is_cuda, f"{name} must be on {device}, a CUDA device")
+    rows, cols = t.shape
+    _need(cols <= 1 or t.stride(1) == 1, f"the columns of {name} must be contiguous")
+    if rows <= 1:
+        return max(cols, 1)
+    _need(t.stride(0) >= cols, f"the rows of {name} may not overlap")
+    return t.stride(0)
+
+
+def _vector(t: torch.Tensor, name: str, dtype, n: int, device):
+    _need(t.dim() == 1 and t.dtype == dtype and t.shape[0] == n and t.is_contiguous(),
+          f"{name} must be a contiguous vector of {n} {dtype}")
+    _need(t.device == device, f"{name} must be on {device}")
+
+
+def _output(out, rows: int, cols: int, dtype, device):
+    if out is None:
+        _need(dtype in _DTYPE, f"unsupported output type {dtype}")
+        out = torch.empty((rows, cols), dtype=dtype, device=device)
+        return out, max(cols, 1)
+    ld = _matrix(out, "out", tuple(_DTYPE), device)
+    _need(tuple(out.shape) == (rows, cols), f"out must be {rows} x {cols}")
+    return out, ld
+
+
+def _scratch(nbytes: int, device, given: Optional[torch.Tensor]):
+    """The workspace of a call whose status word the caller clears: pointer, size, owner."""
+    if given is not None:
+        _need(given.device == device and given.is_contiguous(), f"workspace must be contiguous, on {device}")
+        return given.data_ptr(), given.numel() * given.element_size(), given
+    if nbytes == 0:
+        return 0, 0, None
+    t = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    return t.data_ptr(), nbytes, t
+
+
+class _On:
+    """Make `device` current for a call if it is not."""
+    __slots__ = ("ctx",)
+
+    def __init__(self, device):
+        self.ctx = None if torch.cuda.current_device() == device.index else torch.cuda.device(device)
+
+    def __enter__(self):
+        if self.ctx is not None:
+            self.ctx.__enter__()
+
+    def __exit__(self, *exc):
+        if self.ctx is not None:
+            self.ctx.__exit__(*exc)
+
+
+class Int8Layer:
+    """A linear layer in 8-bit integers: weight int8 [N][Kin] (rows 16-byte
+    aligned, a stride that is a multiple of 16), one float32 scale per output
+    channel, optional float16 output bias.  ``quantise`` makes one from a
+    float16 or bfloat16 matrix."""
+
+    def __init__(self, weight: torch.Tensor, scale: torch.Tensor, out_bias: Optional[torch.Tensor] = None):
+        ld = _matrix(weight, "weight", (torch.int8,), weight.device)
+        n, k = weight.shape
+        _vector(scale, "scale", torch.float32, n, weight.device)
+        if out_bias is not None:
+            _vector(out_bias, "out_bias", torch.float16, n, weight.device)
+        self.weight, self.scale, self.out_bias = weight, scale, out_bias
+        self.out_features, self.in_features, self.device = n, k, weight.device
+        d = _I8Desc()
+        d.out_features, d.in_features = n, k
+        d.w, d.ldw = weight.data_ptr(), ld if n > 1 else -(-max(k, 1) // 16) * 16
+        d.scale = scale.data_ptr()
+        d.out_bias = None if out_bias is None else out_bias.data_ptr()
+        self._desc = d
+        self._ref = C.addressof(d)
+        self._need = {}
+
+    @classmethod
+    def quantise(cls, w: torch.Tensor, out_bias: Optional[torch.Tensor] = None) -> "Int8Layer":
+        """From W [N][Kin] (float16 or bfloat16, on the device), row by row (vq_quant_i8)."""
+        q, scale = quant_i8(w)
+        return cls(q, scale, out_bias)
+
+    def nbytes(self) -> int:
+        return self.weight.shape[0] * (self.weight.shape[1] + 4 + (0 if self.out_bias is None else 2))
+
+    def _bytes(self, fn: str, m: int) -> int:
+        """Workspace bytes of vq_<fn>_i8 for m rows."""
+        n = C.c_size_t(0)
+        name = f"vq_{fn}_i8_workspace_size"
+        _check(name, getattr(lib(), name)(self._ref, m, C.byref(n)))
+        return n.value
+
+
+def gemm_i8_workspace_size(layer: Int8Layer, m: int) -> int:
+    return layer._bytes("gemm", m)
+
+
+def linear_i8_workspace_size(layer: Int8Layer, m: int) -> int:
+    return layer._bytes("linear", m)
+
+
+def quant_i8(x: torch.Tensor, out: Optional[torch.Tensor] = None, scale: Optional[torch.Tensor] = None):
+    """(q, scale): the rows of x (bf16 or fp16 [m][n]) as int8 with one float32
+    scale each (vq_quant_i8).  A new q has rows padded to 16 bytes, as gemm_i8
+    and Int8Layer want them."""
+    dev = x.device
+    ldx = _matrix(x, "x", _IN16, dev)
+    m, n = x.shape
+    if out is None:
+        ldq = -(-max(n, 1) // 16) * 16
+        out = torch.empty((m, ldq), dtype=torch.int8, device=dev)
+        if ldq != n:
+            out = out[:, :n]
+    else:
+        ldq = _matrix(out, "out", (torch.int8,), dev)
+        _need(out.shape == x.shape, "out must have x's shape")
+    if scale is None:
+        scale = torch.empty(m, dtype=torch.float32, device=dev)
+    else:
+        _vector(scale, "scale", torch.float32, m, dev)
+    with _On(dev):
+        _check("vq_quant_i8", lib().vq_quant_i8(x.data_ptr(), _DTYPE[x.dtype], m, n, ldx, out.data_ptr(), ldq,
+                                                scale.data_ptr(), _stream(dev)))
+    return out, scale
+
+
+def gemm_i8(layer: Int8Layer, q: torch.Tensor, q_scale: torch.Tensor, out_dtype=torch.bfloat16,
+            out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """y [m][N] = (q . W^T) * scale * q_scale + bias for rows that quant_i8 made (vq_gemm_i8)."""
+    dev = layer.device
+    ldq = _matrix(q, "q", (torch.int8,), dev)
+    m, k = q.shape
+    _need(k == layer.in_features, f"q must have {layer.in_features} columns")
+    if m <= 1:
+        ldq = -(-ldq // 16) * 16
+    _vector(q_scale, "q_scale", torch.float32, m, dev)
+    out, ldy = _output(out, m, layer.out_features, out_dtype, dev)
+    with _On(dev):
+        ws, n, keep = _scratch(layer._bytes("gemm", m), dev, workspace)
+        _check("vq_gemm_i8", lib().vq_gemm_i8(layer._ref, q.data_ptr(), ldq, q_scale.data_ptr(), m, out.data_ptr(),
+                                              _DTYPE[out.dtype], ldy, ws, n, _stream(dev)))
+    return out
+
+
+def linear_i8(layer: Int8Layer, x: torch.Tensor, out_dtype=torch.bfloat16, out: Optional[torch.Tensor] = None,
+              workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """y [m][N] of bf16 or fp16 activations x [m][Kin]: quant_i8 and gemm_i8 in one call (vq_linear_i8)."""
+    dev = layer.device
+    ldx = _matrix(x, "x", _IN16, dev)
+    m, k = x.shape
+    _need(k == layer.in_features, f"x must have {layer.in_features} columns")
+    out, ldy = _output(out, m, layer.out_features, out_dtype, dev)
+    with _On(dev):
+        ws, n, keep = _scratch(layer._bytes("linear", m), dev, workspace)
+        _check("vq_linear_i8", lib().vq_linear_i8(layer._ref, x.data_ptr(), _DTYPE[x.dtype], m, ldx, out.data_ptr(),
+                                                  _DTYPE[out.dtype], ldy, ws, n, _stream(dev)))
+    return out
+
+
+# ---------------------------------------------------------------------------
+# The experts of a mixture (include/vq_experts.h).
+# ---------------------------------------------------------------------------
+class Experts:
+    """Codebook-indexed experts of one shape, stacked: ``idx[m]`` int32
+    [E][N][row_words] (row order) or [E][tiles][tile_words] (tiled),
+    ``codebooks[m]`` float16 [E][K][d] or [1][K][d] (one book for all), scale,
+    bias and out_bias float16 [E][N] or [1][N].  ``from_layers`` stacks
+    ``Layer`` objects; ``layer(e)`` is expert e as a ``Layer`` on the same
+    memory."""
+
+    def __init__(self, out_features: int, in_features: int, vec_dim: int, log2k: Sequence[int],
+                 idx: Sequence[torch.Tensor], codebooks: Sequence[torch.Tensor], scale: Optional[torch.Tensor] = None,
+                 bias: Optional[torch.Tensor] = None, layout: str = "rows", out_bias: Optional[torch.Tensor] = None):
+        _need(layout in _LAYOUT, f"unknown index layout {layout!r}")
+        _need(1 <= len(log2k) <= 2 and len(idx) == len(log2k) == len(codebooks),
+              "one or two books, an index stream and a codebook each")
+        _need(idx[0].dim() == 3 and idx[0].is_cuda, "idx must be stacked streams on a CUDA device")
+        _need(1 <= vec_dim <= 16 and all(1 <= int(b) <= 16 for b in log2k), "vec_dim and log2k must lie in 1..16")
+        dev, e = idx[0].device, idx[0].shape[0]
+        nvec = -(-in_features // vec_dim)
+        stream_rows = out_features if layout == "rows" else -(-nvec // 4)
+        D = _ExpertsDesc()
+        d = D.layer
+        d.out_features, d.in_features, d.vec_dim, d.n_books = out_features, in_features, vec_dim, len(log2k)
+        d.idx_layout = _LAYOUT[layout]
+        for m, b in enumerate(log2k):
+            t, c = idx[m], codebooks[m]
+            _need(t.dtype == torch.int32 and t.device == dev and tuple(t.shape[:2]) == (e, stream_rows)
+                  and (t.shape[2] <= 1 or t.stride(2) == 1),
+                  f"idx[{m}] must be int32 [{e}][{stream_rows}][words], its words contiguous, on {dev}")
+            _need(c.dtype == torch.float16 and c.device == dev and c.dim() == 3 and c.shape[0] in (1, e)
+                  and tuple(c.shape[1:]) == (1 << int(b), vec_dim) and c[0].is_contiguous(),
+                  f"codebooks[{m}] must be float16 [{e} or 1][{1 << int(b)}][{vec_dim}], each book contiguous, on {dev}")
+            d.log2k[m], d.idx[m], d.codebook[m] = int(b), t.data_ptr(), c.data_ptr()
+            d.idx_row_words[m] = t.stride(1) if stream_rows > 1 and t.shape[2] > 0 else t.shape[2]
+            words = row_words(in_features, vec_dim, int(b)) if layout == "rows" else tile4_words(out_features, int(b))
+            _need(words <= t.shape[2] <= d.idx_row_words[m] or stream_rows == 0 or t.shape[1] == 0,
+                  f"idx[{m}] needs {words} words a row, and rows that do not overlap")
+            D.idx_stride[m] = t.stride(0) if e > 1 and t.numel() > 0 else 0
+            D.codebook_stride[m] = c.stride(0) if c.shape[0] > 1 else 0
+        for name, t in (("scale", scale), ("bias", bias), ("out_bias", out_bias)):
+            if t is None:
+                continue
+            _need(t.dtype == torch.float16 and t.device == dev and t.dim() == 2 and t.shape[0] in (1, e)
+                  and t.shape[1] == out_features and (out_features <= 1 or t.stride(1) == 1),
+                  f"{name} must be float16 [{e} or 1][{out_features}] on {dev}")
+            setattr(d, name, t.data_ptr())
+            setattr(D, name + "_stride", t.stride(0) if t.shape[0] > 1 else 0)
+        D.n_experts = e
+        self.n_experts, self.out_features, self.in_features, self.vec_dim = e, out_features, in_features, vec_dim
+        self.log2k, self.layout, self.device = [int(b) for b in log2k], layout, dev
+        self.idx, self.codebooks = list(idx), list(codebooks)
+        self.scale, self.bias, self.out_bias = scale, bias, out_bias
+        self._desc = D
+        self._ref = C.addressof(D)
+
+    @classmethod
+    def from_layers(cls, layers: Sequence[Layer]) -> "Experts":
+        """Stack layers of one shape, layout and device (their tensors are copied)."""
+        a = layers[0]
+        shape = lambda l: (l.out_features, l.in_features, l.vec_dim, list(l.log2k), l.layout, l.device,
+                           [tuple(t.shape) for t in l.idx], l.scale is None, l.bias is None, l.out_bias is None)
+        _need(all(shape(l) == shape(a) for l in layers), "the layers must have one shape, layout and device")
+        books = []
+        for m in range(a.n_books):
+            size = a.codebooks[m].numel()
+            # every book starts on 16 bytes
+            flat = torch.zeros((len(layers), -(-size // 8) * 8), dtype=torch.float16, device=a.device)
+            for e, l in enumerate(layers):
+                flat[e, :size] = l.codebooks[m].reshape(-1)
+            books.append(flat.as_strided((len(layers), 1 << a.log2k[m], a.vec_dim), (flat.shape[1], a.vec_dim, 1)))
+        stack = lambda ts: None if ts[0] is None else torch.stack(ts)
+        return cls(a.out_features, a.in_features, a.vec_dim, a.log2k,
+                   [torch.stack([l.idx[m] for l in layers]) for m in range(a.n_books)], books,
+                   stack([l.scale for l in layers]), stack([l.bias for l in layers]), a.layout,
+                   stack([l.out_bias for l in layers]))
+
+    def layer(self, e: int) -> Layer:
+        at = lambda t: None if t is None else t[e if t.shape[0] > 1 else 0]
+        return Layer(self.out_features, self.in_features, self.vec_dim, list(self.log2k), [t[e] for t in self.idx],
+                     [at(c) for c in self.codebooks], at(self.scale), at(self.bias), layout=self.layout,
+                     out_bias=at(self.out_bias))
+
+    def nbytes(self) -> int:
+        return sum(t.numel() * t.element_size() for t in
+                   self.idx + self.codebooks + [v for v in (self.scale, self.bias, self.out_bias) if v is not None])
+
+
+def group_rows(ids: torch.Tensor, n_experts: int, offsets: Optional[torch.Tensor] = None,
+               rows: Optional[torch.Tensor] = None, pos: Optional[torch.Tensor] = None):
+    """(offsets [E+1], rows [T * top_k], pos [T][top_k]) of the picks ids (int32
+    [T][top_k]) in the order of their experts (vq_group_rows)."""
+    dev = ids.device
+    ld = _matrix(ids, "ids", (torch.int32,), dev)
+    t, k = ids.shape
+    if offsets is None:
+        offsets = torch.empty(max(n_experts, 0) + 1, dtype=torch.int32, device=dev)
+    else:
+        _vector(offsets, "offsets", torch.int32, n_experts + 1, dev)
+    if rows is None:
+        rows = torch.empty(t * k, dtype=torch.int32, device=dev)
+    else:
+        _vector(rows, "rows", torch.int32, t * k, dev)
+    if pos is None:
+        pos = torch.empty((t, k), dtype=torch.int32, device=dev)
+    else:
+        _need(pos.dtype == torch.int32 and pos.device == dev and pos.shape == ids.shape and pos.is_contiguous(),
+              "pos must be contiguous int32 of ids' shape")
+    with _On(dev):
+        _check("vq_group_rows", lib().vq_group_rows(ids.data_ptr(), t, k, ld, n_experts, offsets.data_ptr(),
+                                                    rows.data_ptr(), pos.data_ptr(), _stream(dev)))
+    return offsets, rows, pos
+
+
+def gemm_experts_workspace_size(experts: Experts, m: int) -> int:
+    n = C.c_size_t(0)
+    _check("vq_gemm_experts_workspace_size", lib().vq_gemm_experts_workspace_size(experts._ref, m, C.byref(n)))
+    return n.value
+
+
+def gemm_experts(experts: Experts, x: torch.Tensor, offsets: torch.Tensor, rows: Optional[torch.Tensor] = None,
+                 out_dtype=torch.bfloat16, out: Optional[torch.Tensor] = None,
+                 workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """y [m][N]: rows offsets[e] .. offsets[e+1]-1 are the products of their
+    rows of x with expert e (vq_gemm_experts).  Grouped row r reads x[rows[r]],
+    or x[r] without ``rows``; m is the length of ``rows``, else of x.  Rows
+    behind the last group are not written."""
+    dev = experts.device
+    ldx = _matrix(x, "x", _IN16, dev)
+    _need(x.shape[1] == experts.in_features, f"x must have {experts.in_features} columns")
+    _vector(offsets, "offsets", torch.int32, experts.n_experts + 1, dev)
+    m = x.shape[0]
+    if rows is not None:
+        _need(rows.dim() == 1, "rows must be a vector")
+        m = rows.shape[0]
+        _vector(rows, "rows", torch.int32, m, dev)
+    out, ldy = _output(out, m, experts.out_features, out_dtype, dev)
+    with _On(dev):
+        ws, n, keep = _scratch(gemm_experts_workspace_size(experts, m), dev, workspace)
+        _check("vq_gemm_experts", lib().vq_gemm_experts(
+            experts._ref, x.data_ptr(), _DTYPE[x.dtype], x.shape[0], ldx, None if rows is None else rows.data_ptr(),
+            offsets.data_ptr(), m, out.data_ptr(), _DTYPE[out.dtype], ldy, ws, n, _stream(dev)))
+    return out
+
+
+def combine_rows(z: torch.Tensor, pos: torch.Tensor, weight: torch.Tensor, out_dtype=torch.bfloat16,
+                 out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """y [T][n] = sum_j weight[t][j] z[pos[t][j]] over a token's picks (vq_combine_rows)."""
+    dev = z.device
+    ldz = _matrix(z, "z", tuple(_DTYPE), dev)
+    _need(pos.dim() == 2 and pos.dtype == torch.int32 and pos.device == dev and pos.is_contiguous(),
+          f"pos must be a contiguous int32 matrix on {dev}")
+    t, k = pos.shape
+    ldw = _matrix(weight, "weight", (torch.float32,), dev)
+    _need(weight.shape == pos.shape, "weight must have pos's shape")
+    out, ldy = _output(out, t, z.shape[1], out_dtype, dev)
+    with _On(dev):
+        _check("vq_combine_rows", lib().vq_combine_rows(
+            z.data_ptr(), _DTYPE[z.dtype], z.shape[0], z.shape[1], ldz, pos.data_ptr(), weight.data_ptr(), ldw, t, k,
+            out.data_ptr(), _DTYPE[out.dtype], ldy, _stream(dev)))
+    return out
 
 
 def kernel_launches() -> int:
