@@ -9,9 +9,10 @@
 // multiply-add gives exactly (its only rounding cannot change a sign).  One
 // element in 5000 takes that path; the kernel stays at the memory's speed.
 #include <algorithm>
+#include <cstdlib>
 
+#include "sm100.cuh"
 #include "vq_i8.h"
-#include "vq_internal.cuh"
 
 namespace vqk {
 namespace {
@@ -65,6 +66,8 @@ __global__ void __launch_bounds__(1024) quant_i8_kernel(const uint16_t* __restri
                                                         int8_t* __restrict__ q, int64_t ldq,
                                                         float* __restrict__ scale) {
   __shared__ uint32_t s_top[32];
+  // the product after this kernel may start loading its weights
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int64_t row = blockIdx.x;
   const uint16_t* xr = x + row * ldx;
   int8_t* qr = q + row * ldq;
@@ -157,8 +160,17 @@ cudaError_t launch_quant(const uint16_t* x, int rows, int n, int64_t ldx, int8_t
 }
 
 // ---------------------------------------------------------------------------
-// Product.
+// Product: y^T = W q^T on the integer tensor cores (tcgen05 kind::i8, exact
+// 32-bit sums).  W's rows are the MMA's M and the activations' rows its N, so
+// that one token and four thousand take the same path: a decode step is W
+// streamed once past a narrow N.  Both operands come by TMA as 128-byte
+// swizzled rows (128 values of k a step); rows and columns past the matrices
+// read as zeros.  A thread of the epilogue owns one output channel, so its
+// scale and bias are registers and a warp stores 32 neighbouring outputs of a
+// token at a time.
 // ---------------------------------------------------------------------------
+using namespace sm100;
+
 struct I8Layer {
   int n, kin;
   const int8_t* w;
@@ -167,46 +179,349 @@ struct I8Layer {
   const uint16_t* ob;
 };
 
-constexpr int kTile = 64;     // outputs and rows of a block
-constexpr int kStep = 64;     // bytes of k per step
+struct I8Args {
+  int n, m;               // outputs, activation rows
+  int num_kt;             // steps of 128 values
+  int tn;                 // activation rows per tile (MMA N)
+  const float* ws;        // weight scales
+  const uint16_t* ob;
+  const float* qs;        // activation scales
+  void* y;
+  vq_dtype yt;
+  int64_t ldy;
+  int* status;
+  long long budget;
+  int kt_per_split;       // narrow kernel: steps of a CTA of the cluster
+  int tiles_n, tiles_m;   // wide kernel: tiles of 256 outputs, of tn rows
+  int stages;
+};
 
-// y tile of 64 rows x 64 outputs per block of 256 threads, four by four per
-// thread, dp4a on words staged in shared memory.
-__global__ void __launch_bounds__(256) gemm_i8_kernel(I8Layer L, const int8_t* __restrict__ q, int64_t ldq,
-                                                      const float* __restrict__ qs, int m, void* __restrict__ y,
-                                                      vq_dtype yt, int64_t ldy) {
-  __shared__ int sa[kTile][kStep / 4 + 1], sb[kTile][kStep / 4 + 1];
-  const int o0 = blockIdx.x * kTile, i0 = blockIdx.y * kTile;
-  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-  int acc[4][4] = {};
-  for (int k0 = 0; k0 < L.kin; k0 += kStep) {
-    for (int w = threadIdx.x; w < kTile * (kStep / 4); w += 256) {
-      const int r = w / (kStep / 4), c = w % (kStep / 4);
-      const int k = k0 + 4 * c;
-      int a = 0, b = 0;
-      if (k < L.kin) {
-        const int keep = min(4, L.kin - k);
-        const uint32_t mask = keep == 4 ? 0xFFFFFFFFu : (1u << (8 * keep)) - 1u;
-        if (i0 + r < m) a = *reinterpret_cast<const int*>(q + (i0 + r) * ldq + k) & mask;
-        if (o0 + r < L.n) b = *reinterpret_cast<const int*>(L.w + (o0 + r) * L.ldw + k) & mask;
-      }
-      sa[r][c] = a;
-      sb[r][c] = b;
+constexpr int kRows = 128;                 // output channels per CTA
+constexpr int kStepBytes = 128;            // values of k per step
+constexpr int kWTile = kRows * kStepBytes;
+constexpr int kMaxStages = 8;
+constexpr long long kDrain = 1LL << 26;    // SM clocks: far above any load's latency
+
+__device__ __forceinline__ uint8_t* align1024(uint8_t* p) {
+  return reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(p) + 1023) & ~uintptr_t(1023));
+}
+__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+// One output from its exact sum.
+__device__ __forceinline__ float i8_out(int acc, float w, float s, float b) {
+  return __fadd_rn(__fmul_rn(__fmul_rn(__int2float_rn(acc), w), s), b);
+}
+
+// ---- one to 64 rows: W's bytes are the bound ------------------------------------
+// A cluster of S CTAs shares a tile of 128 outputs, each CTA a run of k, so
+// that even a layer of 1024 outputs keeps most SMs loading.  The partial sums
+// meet in distributed shared memory: integers, so the split changes nothing
+// in y, and no workspace, counter or second launch is needed.
+struct NarrowCtrl {
+  uint64_t full[kMaxStages], empty[kMaxStages], acc;
+  uint32_t tmem;
+  int abort;
+};
+constexpr int kNarrowRows = 64;
+constexpr int kNarrowThreads = 192;        // warp 0: loads, warp 1: products, warps 2-5: epilogue
+
+__global__ void __launch_bounds__(kNarrowThreads) gemm_i8_narrow_kernel(const __grid_constant__ CUtensorMap wmap,
+                                                                        const __grid_constant__ CUtensorMap xmap,
+                                                                        I8Args g) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* base = align1024(smem_raw);
+  NarrowCtrl* ctrl = reinterpret_cast<NarrowCtrl*>(base);
+  uint8_t* stages = base + 1024;
+  const int stage = kWTile + g.tn * kStepBytes;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int splits = gridDim.y, split = blockIdx.y;          // the cluster spans the grid's y
+  const int row0 = blockIdx.x * kRows;
+  const int kt0 = split * g.kt_per_split;
+  const int nkt = max(0, min(g.num_kt, kt0 + g.kt_per_split) - kt0);
+  volatile int* abort_flag = &ctrl->abort;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < g.stages; ++s) {
+      mbar_init(&ctrl->full[s], 1);
+      mbar_init(&ctrl->empty[s], 1);
     }
-    __syncthreads();
-    for (int c = 0; c < kStep / 4; ++c)
+    mbar_init(&ctrl->acc, 1);
+    ctrl->abort = 0;
+    fence_barrier_init();
+    // the first weight tiles do not wait for the kernel before this one (the
+    // quantisation of the activations)
+    for (int i = 0; i < min(nkt, g.stages); ++i) {
+      mbar_arrive_expect_tx(&ctrl->full[i], stage);
+      tma_load_2d(stages + i * stage, &wmap, &ctrl->full[i], (kt0 + i) * kStepBytes, row0);
+    }
+  }
+  if (warp == 1) {
+    tmem_alloc(&ctrl->tmem, 64);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = ctrl->tmem;
+  pdl_wait();
+
+  if (warp == 0) {
+    if (lane == 0) {
+      int issued = min(nkt, g.stages);
+      for (int i = 0; i < issued; ++i)
+        tma_load_2d(stages + i * stage + kWTile, &xmap, &ctrl->full[i], (kt0 + i) * kStepBytes, 0);
+      for (int i = issued; i < nkt; ++i) {
+        const int s = i % g.stages;
+        if (!bounded_wait(&ctrl->empty[s], ((i / g.stages) & 1) ^ 1, abort_flag, g.status, g.budget)) break;
+        mbar_arrive_expect_tx(&ctrl->full[s], stage);
+        tma_load_2d(stages + s * stage, &wmap, &ctrl->full[s], (kt0 + i) * kStepBytes, row0);
+        tma_load_2d(stages + s * stage + kWTile, &xmap, &ctrl->full[s], (kt0 + i) * kStepBytes, 0);
+        issued = i + 1;
+      }
+      if (*abort_flag)                                       // loads in flight land before the block ends
+        for (int i = max(0, issued - g.stages); i < issued; ++i)
+          drain_phase(&ctrl->full[i % g.stages], (i / g.stages) & 1, kDrain);
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      const uint32_t idesc = i8_idesc(kRows, g.tn);
+      for (int i = 0; i < nkt; ++i) {
+        const int s = i % g.stages;
+        if (!bounded_wait(&ctrl->full[s], (i / g.stages) & 1, abort_flag, g.status, g.budget)) break;
+        tc_fence_after();
+        const uint32_t a = smem_addr(stages + s * stage);
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+        for (int kk = 0; kk < kStepBytes / 32; ++kk)
+          umma_i8(tmem, sw128_kmajor_desc(a + kk * 32), sw128_kmajor_desc(a + kWTile + kk * 32), idesc, (i | kk) != 0);
+        umma_commit(&ctrl->empty[s]);
+      }
+      umma_commit(&ctrl->acc);
+      drain_phase(&ctrl->acc, 0, kDrain);                    // nothing runs in tensor memory after this
+    }
+  } else {
+    const int lq = warp & 3, r = 32 * lq + lane, o = row0 + r;
+    const bool ok = __all_sync(0xffffffffu, bounded_wait(&ctrl->acc, 0, abort_flag, g.status, g.budget));
+    tc_fence_after();
+    const uint32_t t = tmem + (static_cast<uint32_t>(32 * lq) << 16);
+    if (splits == 1) {
+      const bool live = ok && o < g.n;
+      const float w = live ? g.ws[o] : 0.0f, b = live ? out_bias_of(g.ob, o) : 0.0f;
+      for (int c = 0; c < g.m; c += 16) {
+        uint32_t acc[16];
+        tmem_ld16(t + c, acc);
+        tmem_wait_ld();
 #pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = __dp4a(sa[ty + 16 * i][c], sb[tx + 16 * j][c], acc[i][j]);
+        for (int i = 0; i < 16; ++i)
+          if (live && c + i < g.m)
+            store_out(g.y, g.yt, (c + i) * g.ldy + o, i8_out(nkt ? static_cast<int>(acc[i]) : 0, w, __ldg(g.qs + c + i), b));
+      }
+    } else if (ok) {
+      // partial sums to the (spent) stage memory, [row of x][128]
+      int* red = reinterpret_cast<int*>(stages);
+      for (int c = 0; c < g.m; c += 16) {
+        uint32_t acc[16];
+        tmem_ld16(t + c, acc);
+        tmem_wait_ld();
+#pragma unroll
+        for (int i = 0; i < 16; ++i) red[(c + i) * kRows + r] = nkt ? static_cast<int>(acc[i]) : 0;
+      }
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  if (splits > 1) {
+    cluster_arrive();
+    cluster_wait();
+    // this CTA's share of the tile's outputs
+    const int total = g.m * kRows, share = (total + splits - 1) / splits;
+    const int last = min(total, (split + 1) * share);
+    if (!*abort_flag) {
+      for (int i = split * share + threadIdx.x; i < last; i += kNarrowThreads) {
+        const int* mine = reinterpret_cast<const int*>(stages) + i;
+        int sum = 0;
+        for (int s = 0; s < splits; ++s) {
+          int v;
+          asm volatile("ld.shared::cluster.b32 %0, [%1];" : "=r"(v) : "r"(cluster_addr(mine, s)) : "memory");
+          sum += v;
+        }
+        const int c = i / kRows, o = row0 + (i & (kRows - 1));
+        if (o < g.n) store_out(g.y, g.yt, c * g.ldy + o, i8_out(sum, g.ws[o], __ldg(g.qs + c), out_bias_of(g.ob, o)));
+      }
+    }
+    cluster_arrive();                                        // no CTA leaves while others read its sums
+    cluster_wait();
+  } else {
     __syncthreads();
   }
-  for (int i = 0; i < 4; ++i)
-    for (int j = 0; j < 4; ++j) {
-      const int r = i0 + ty + 16 * i, o = o0 + tx + 16 * j;
-      if (r < m && o < L.n)
-        store_out(y, yt, r * ldy + o, (__int2float_rn(acc[i][j]) * L.scale[o]) * qs[r] + out_bias_of(L.ob, o));
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 64);
+  }
+}
+
+// ---- more rows: the tensor cores are the bound ----------------------------------
+// Persistent pairs of CTAs (cta_group::2): a tile is 256 outputs by up to 256
+// rows, each CTA loading 128 rows of W and half the rows of q per step, so
+// that shared memory feeds the products at half the bytes a lone CTA would
+// need.  Two accumulators alternate in tensor memory: the epilogue of a tile
+// runs under the products of the next.
+struct WideCtrl {
+  uint64_t full[kMaxStages], empty[kMaxStages];
+  uint64_t accf[2], acce[2];
+  uint32_t tmem;
+  int abort;
+};
+constexpr int kWideThreads = 256;          // warp 0: loads, warp 1: products, warps 4-7: epilogue
+constexpr int kWideTn = 256;
+constexpr uint32_t kWideCols = 512;
+
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1)
+    gemm_i8_wide_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap, I8Args g) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* base = align1024(smem_raw);
+  WideCtrl* ctrl = reinterpret_cast<WideCtrl*>(base);
+  uint8_t* stages = base + 1024;
+  const int half = g.tn / 2;                                 // rows of q per CTA
+  const int stage = kWTile + half * kStepBytes;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_ctarank();
+  const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+  const int tiles = g.tiles_n * g.tiles_m;
+  volatile int* abort_flag = &ctrl->abort;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < g.stages; ++s) {
+      mbar_init(&ctrl->full[s], 1);
+      mbar_init(&ctrl->empty[s], 1);
     }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&ctrl->accf[b], 1);
+      mbar_init(&ctrl->acce[b], 8);                          // the epilogue warps of both CTAs
+    }
+    ctrl->abort = 0;
+    fence_barrier_init();
+    tma_prefetch(&wmap);
+    tma_prefetch(&xmap);
+  }
+  if (warp == 2) {
+    tmem_alloc_pair(&ctrl->tmem, kWideCols);
+    tmem_relinquish_pair();
+  }
+  tc_fence_before();
+  cluster_arrive();                                          // both CTAs' barriers exist
+  cluster_wait();
+  tc_fence_after();
+  const uint32_t tmem = ctrl->tmem;
+  pdl_wait();
+
+  if (warp == 0) {
+    if (lane == 0) {
+      int gs = 0;
+      bool stop = false;
+      for (int tile = pair; tile < tiles && !stop; tile += pairs) {
+        const int row0 = (tile / g.tiles_m) * 2 * kRows + rank * kRows;
+        const int t0 = (tile % g.tiles_m) * g.tn + rank * half;
+        for (int i = 0; i < g.num_kt; ++i, ++gs) {
+          const int s = gs % g.stages;
+          if (!bounded_wait(&ctrl->empty[s], ((gs / g.stages) & 1) ^ 1, abort_flag, g.status, g.budget)) {
+            stop = true;
+            break;
+          }
+          const uint32_t bar = cluster_addr(&ctrl->full[s], 0);
+          if (rank == 0) mbar_arrive_expect_tx(&ctrl->full[s], 2 * stage);
+          tma_load_2d_pair(stages + s * stage, &wmap, bar, i * kStepBytes, row0);
+          tma_load_2d_pair(stages + s * stage + kWTile, &xmap, bar, i * kStepBytes, t0);
+        }
+      }
+      // the last products' arrivals on this CTA's barriers are in
+      for (int i = max(0, gs - g.stages); i < gs && !*abort_flag; ++i)
+        bounded_wait(&ctrl->empty[i % g.stages], (i / g.stages) & 1, abort_flag, g.status, g.budget);
+      if (*abort_flag) {
+        // Loads in flight land before the block ends.  Their barriers may
+        // never complete once one CTA of the pair has given up, so time does.
+        const long long t0 = clock64();
+        while (clock64() - t0 < kDrain / 16) __nanosleep(1000);
+      }
+    }
+  } else if (warp == 1) {
+    if (lane == 0 && rank == 0) {
+      const uint32_t idesc = i8_idesc(2 * kRows, g.tn);
+      int gs = 0, it = 0;
+      bool stop = false;
+      for (int tile = pair; tile < tiles && !stop; tile += pairs, ++it) {
+        const int buf = it & 1;
+        if (it >= 2 && !bounded_wait(&ctrl->acce[buf], ((it >> 1) & 1) ^ 1, abort_flag, g.status, g.budget)) break;
+        tc_fence_after();
+        for (int i = 0; i < g.num_kt; ++i, ++gs) {
+          const int s = gs % g.stages;
+          if (!bounded_wait(&ctrl->full[s], (gs / g.stages) & 1, abort_flag, g.status, g.budget)) {
+            stop = true;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t a = smem_addr(stages + s * stage);
+#pragma unroll
+          for (int kk = 0; kk < kStepBytes / 32; ++kk)
+            umma_i8_pair(tmem + buf * kWideTn, sw128_kmajor_desc(a + kk * 32), sw128_kmajor_desc(a + kWTile + kk * 32),
+                         idesc, (i | kk) != 0);
+          umma_commit_pair(&ctrl->empty[s]);
+        }
+        if (!stop) umma_commit_pair(&ctrl->accf[buf]);
+      }
+      if (*abort_flag) {                                     // products in flight end before tensor memory is freed
+        const long long t0 = clock64();
+        while (clock64() - t0 < kDrain / 16) __nanosleep(1000);
+      }
+    }
+  } else if (warp >= 4) {
+    const int lq = warp & 3;
+    int it = 0;
+    for (int tile = pair; tile < tiles; tile += pairs, ++it) {
+      const int buf = it & 1;
+      const int o = (tile / g.tiles_m) * 2 * kRows + rank * kRows + 32 * lq + lane;
+      const int t0 = (tile % g.tiles_m) * g.tn;
+      const bool live = o < g.n;
+      const float w = live ? __ldg(g.ws + o) : 0.0f, b = live ? out_bias_of(g.ob, o) : 0.0f;
+      if (!__all_sync(0xffffffffu, bounded_wait(&ctrl->accf[buf], (it >> 1) & 1, abort_flag, g.status, g.budget))) break;
+      tc_fence_after();
+      const int cols = min(g.tn, g.m - t0);
+      for (int c = 0; c < cols; c += 32) {
+        uint32_t acc[32];
+        tmem_ld32(tmem + buf * kWideTn + c + (static_cast<uint32_t>(32 * lq) << 16), acc);
+        const float sl = t0 + c + lane < g.m ? __ldg(g.qs + t0 + c + lane) : 0.0f;
+        tmem_wait_ld();
+        const int n = min(32, cols - c);
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+          const float s = __shfl_sync(0xffffffffu, sl, i);
+          if (live && i < n)
+            store_out(g.y, g.yt, static_cast<int64_t>(t0 + c + i) * g.ldy + o, i8_out(static_cast<int>(acc[i]), w, s, b));
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(cluster_addr(&ctrl->acce[buf], 0));
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  cluster_arrive();
+  cluster_wait();
+  if (warp == 2) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem, kWideCols);
+  }
+}
+
+// y = bias for a layer without inputs.
+__global__ void i8_bias_kernel(int n, int m, const uint16_t* __restrict__ ob, const float* __restrict__ ws,
+                               const float* __restrict__ qs, void* __restrict__ y, vq_dtype yt, int64_t ldy) {
+  for (int64_t i = blockIdx.x * static_cast<int64_t>(blockDim.x) + threadIdx.x; i < static_cast<int64_t>(m) * n;
+       i += static_cast<int64_t>(gridDim.x) * blockDim.x) {
+    const int64_t r = i / n;
+    const int o = static_cast<int>(i - r * n);
+    store_out(y, yt, r * ldy + o, i8_out(0, ws[o], qs[r], out_bias_of(ob, o)));
+  }
 }
 
 vq_status check_i8(const vq_i8_desc* d, I8Layer* L) {
@@ -241,12 +556,107 @@ LinearLayout linear_layout(const I8Layer& L, int m) {
   return l;
 }
 
+long long wait_budget() {
+  if (const char* env = std::getenv("VQ_WAIT_BUDGET")) return std::atoll(env);
+  return 4000000000LL;
+}
+
+// Splits of the narrow kernel: double the cluster while the grid stays within
+// two CTAs per SM and each CTA keeps at least four steps (512 bytes of k).
+int narrow_splits(int tiles, int num_kt, int sms) {
+  int s = 1;
+  while (s < 8 && tiles * s * 2 <= 2 * sms && num_kt >= 8 * s) s *= 2;
+  return s;
+}
+
+// Rows per tile of the wide kernel: the multiple of 32 that takes the fewest
+// clocks over the last wave of pairs, a step costing 2 tn clocks of the tensor
+// cores or the time its 16 KB of weights and tn / 2 rows take to arrive.
+int wide_rows(int m, int tiles_n, int pairs) {
+  int best = kWideTn;
+  int64_t least = -1;
+  for (int tn = kWideTn; tn >= 32; tn -= 32) {
+    const int64_t tiles = static_cast<int64_t>(tiles_n) * ((m + tn - 1) / tn);
+    const int64_t cost = (tiles + pairs - 1) / pairs * std::max(2 * tn, 320 + tn);
+    if (least < 0 || cost < least) {
+      least = cost;
+      best = tn;
+    }
+  }
+  return best;
+}
+
+// pdl: the kernel before this one on the stream is the quantisation that wrote q.
 vq_status launch_gemm_i8(const I8Layer& L, const int8_t* q, int64_t ldq, const float* qs, int m, void* y, vq_dtype yt,
-                         int64_t ldy, void* ws, cudaStream_t stream) {
+                         int64_t ldy, void* ws, cudaStream_t stream, bool pdl) {
+  const int sms = device_sm_count();
+  if (L.kin == 0) {
+    count_launch();
+    const int64_t total = static_cast<int64_t>(m) * L.n;
+    i8_bias_kernel<<<static_cast<int>(std::min<int64_t>((total + 255) / 256, 8 * sms)), 256, 0, stream>>>(
+        L.n, m, L.ob, L.scale, qs, y, yt, ldy);
+    return cuda_status(cudaGetLastError());
+  }
+  I8Args g{};
+  g.n = L.n;
+  g.m = m;
+  g.num_kt = (L.kin + kStepBytes - 1) / kStepBytes;
+  g.ws = L.scale;
+  g.ob = L.ob;
+  g.qs = qs;
+  g.y = y;
+  g.yt = yt;
+  g.ldy = ldy;
+  g.status = static_cast<int*>(ws);
+  g.budget = wait_budget();
+  const bool narrow = m <= kNarrowRows;
+  int box = 0;
+  if (narrow) {
+    g.tn = (m + 15) / 16 * 16;
+    box = g.tn;
+  } else {
+    g.tiles_n = (L.n + 2 * kRows - 1) / (2 * kRows);
+    g.tn = wide_rows(m, g.tiles_n, sms / 2);
+    g.tiles_m = (m + g.tn - 1) / g.tn;
+    box = g.tn / 2;
+  }
+  CUtensorMap wmap, xmap;
+  if (!make_map_u8_sw128(&wmap, L.w, L.kin, L.n, L.ldw, kRows) || !make_map_u8_sw128(&xmap, q, L.kin, m, ldq, box))
+    return VQ_ERR_CUDA;
+  const int stage = kWTile + box * kStepBytes;
+  cudaLaunchConfig_t cfg = {};
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = pdl ? 1 : 0;
+  const void* k;
+  if (narrow) {
+    const int tiles = (L.n + kRows - 1) / kRows;
+    const int splits = narrow_splits(tiles, g.num_kt, sms);
+    g.kt_per_split = (g.num_kt + splits - 1) / splits;
+    g.stages = std::min(kMaxStages, (device_smem_optin() / 2 - 2048 - 1024) / stage);   // two CTAs per SM
+    cfg.gridDim = dim3(tiles, splits);
+    cfg.blockDim = dim3(kNarrowThreads);
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = 1;
+    attr[1].val.clusterDim.y = splits;
+    attr[1].val.clusterDim.z = 1;
+    cfg.numAttrs = 2;
+    k = reinterpret_cast<const void*>(gemm_i8_narrow_kernel);
+  } else {
+    g.stages = std::min(kMaxStages, (device_smem_optin() - 2048) / stage);
+    cfg.gridDim = dim3(2 * std::min(g.tiles_n * g.tiles_m, sms / 2));
+    cfg.blockDim = dim3(kWideThreads);
+    k = reinterpret_cast<const void*>(gemm_i8_wide_kernel);
+  }
+  cfg.dynamicSmemBytes = 2048 + static_cast<size_t>(g.stages) * stage;
+  cudaError_t e = set_func_attr(k, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(cfg.dynamicSmemBytes));
+  if (e != cudaSuccess) return cuda_status(e);
   count_launch();
-  gemm_i8_kernel<<<dim3((L.n + kTile - 1) / kTile, (m + kTile - 1) / kTile), 256, 0, stream>>>(L, q, ldq, qs, m, y, yt,
-                                                                                              ldy);
-  return cuda_status(cudaGetLastError());
+  return cuda_status(narrow ? cudaLaunchKernelEx(&cfg, gemm_i8_narrow_kernel, wmap, xmap, g)
+                            : cudaLaunchKernelEx(&cfg, gemm_i8_wide_kernel, wmap, xmap, g));
 }
 
 vq_status check_out(const I8Layer& L, int m, void* y, vq_dtype yt, int64_t ldy) {
@@ -305,7 +715,8 @@ vq_status vq_gemm_i8(const vq_i8_desc* layer, const int8_t* q, int64_t ldq, cons
   if ((L.kin > 0 && (!aligned(q, 16) || ldq % 16 != 0)) || !aligned(q_scale, 4)) return VQ_ERR_ALIGNMENT;
   st = check_workspace(workspace, workspace_bytes, gemm_i8_bytes(L, m));
   if (st != VQ_OK) return st;
-  return launch_gemm_i8(L, q, ldq, q_scale, m, y, y_dtype, ldy, workspace, static_cast<cudaStream_t>(stream));
+  return launch_gemm_i8(L, q, ldq, q_scale, m, y, y_dtype, ldy, workspace, static_cast<cudaStream_t>(stream),
+                        false);
 }
 
 vq_status vq_linear_i8_workspace_size(const vq_i8_desc* layer, int32_t m, size_t* bytes) {
@@ -339,7 +750,7 @@ vq_status vq_linear_i8(const vq_i8_desc* layer, const void* x, vq_dtype x_dtype,
   auto run = x_dtype == VQ_FP16 ? launch_quant<true> : launch_quant<false>;
   st = cuda_status(run(static_cast<const uint16_t*>(x), m, L.kin, ldx, q, lay.ldq, qs, s));
   if (st != VQ_OK) return st;
-  return launch_gemm_i8(L, q, lay.ldq, qs, m, y, y_dtype, ldy, workspace, s);
+  return launch_gemm_i8(L, q, lay.ldq, qs, m, y, y_dtype, ldy, workspace, s, true);
 }
 
 }  // extern "C"

@@ -162,6 +162,9 @@ vq_status launch_gemv(const Layer& L, const GemvPlan& plan, const void* x, bool 
 bool make_map_f16_sw128(CUtensorMap* map, const void* base, int64_t cols, int64_t rows, int64_t ld,
                         int box_rows);
 
+// The same for bytes: box {128, box_rows} (box_rows <= 256).
+bool make_map_u8_sw128(CUtensorMap* map, const void* base, int64_t cols, int64_t rows, int64_t ld, int box_rows);
+
 // Batched decode on the tensor cores (gemvtc.cu): layers with one 2^16-entry
 // d = 8 book, row or tiled order.
 bool plan_gemv_tc(const Layer& L, int batch, size_t ws_cap, GemvPlan* plan);

@@ -232,6 +232,26 @@ def test_streams_and_graphs():
     assert all(torch.equal(a, b) for a, b in zip(got, want))
 
 
+@pytest.mark.parametrize("m,n,k", [(3, 1024, 8192), (40, 300, 512), (200, 1000, 3000)])
+def test_device_waits_give_up_with_a_status(monkeypatch, m, n, k):
+    """A wait whose budget is zero gives up: the call ends, the status word
+    says so and stays set until it is cleared, and the next call is right."""
+    vq = _vq()
+    w, ws, b = _weights(n, k, 2, True)
+    layer = vq.Int8Layer(w, ws, b)
+    q = torch.randint(-127, 128, (m, -(-k // 16) * 16), device="cuda", dtype=torch.int8)[:, :k]
+    one = torch.ones(m, device="cuda")
+    work = torch.zeros(256, dtype=torch.uint8, device="cuda")
+    monkeypatch.setenv("VQ_WAIT_BUDGET", "0")
+    vq.gemm_i8(layer, q, one, workspace=work)
+    torch.cuda.synchronize()
+    assert int(work[:4].view(torch.int32)) == vq.VQ_ERR_TIMEOUT
+    monkeypatch.delenv("VQ_WAIT_BUDGET")
+    y = vq.gemm_i8(layer, q, one, out_dtype=torch.float32, workspace=work)
+    _check(y, q, one, w, ws, b)
+    assert int(work[:4].view(torch.int32)) == vq.VQ_ERR_TIMEOUT
+
+
 def test_binding_checks():
     vq = _vq()
     w, ws, b = _weights(64, 48, 1, True)
