@@ -1,8 +1,10 @@
 // experts.cu -- vq_gemm_experts: products of codebook-indexed experts over the
 // ragged groups of rows that a router made (include/vq_experts.h).
 #include <algorithm>
+#include <cstdlib>
 
 #include "codebook.cuh"
+#include "sm100.cuh"
 #include "vq_experts.h"
 
 namespace vqk {
@@ -30,40 +32,719 @@ __device__ __forceinline__ Layer expert_layer(const Experts& E, int x) {
   return L;
 }
 
-// One grouped row and 128 outputs per block.
-__global__ void __launch_bounds__(128) gemm_experts_kernel(Experts E, const uint16_t* __restrict__ x, int x_fp16,
-                                                           int x_rows, int64_t ldx, const int32_t* __restrict__ rows,
-                                                           const int32_t* __restrict__ offsets, int m,
-                                                           void* __restrict__ y, vq_dtype yt, int64_t ldy) {
-  const int o = blockIdx.x * 128 + threadIdx.x;
-  for (int r = blockIdx.y; r < m; r += gridDim.y) {
-    int ex = -1, last = 0;
-    for (int k = 0; k < E.e && ex < 0; ++k) {
-      last = max(last, min(m, offsets[k + 1]));
-      if (r < last && r >= min(m, max(0, offsets[k]))) ex = k;
-    }
-    if (ex < 0 || o >= E.L.n) continue;
-    const Layer L = expert_layer(E, ex);
-    const int src = rows ? rows[r] : r;
-    const bool live = src >= 0 && src < x_rows;
-    float acc = 0.0f, sum = 0.0f;
-    for (int j = 0; live && j < L.nvec; ++j) {
-      uint32_t i[2];
-      for (int b = 0; b < L.nb; ++b)
-        i[b] = L.layout == VQ_IDX_ROWS
-                   ? load_field(L.idx[b] + o * L.rw[b], static_cast<int64_t>(j) * L.b[b], L.b[b])
-                   : load_field(L.idx[b] + (j >> 2) * L.rw[b], (4 * static_cast<int64_t>(o) + (j & 3)) * L.b[b], L.b[b]);
-      for (int k = 0; k < L.d && j * L.d + k < L.kin; ++k) {
-        const uint16_t u = __ldg(x + src * ldx + j * L.d + k);
-        const float v = x_fp16 ? h2f(u) : bf2f(u);
-        float c = h2f(L.book[0][static_cast<int64_t>(i[0]) * L.d + k]);
-        if (L.nb == 2) c += h2f(L.book[1][static_cast<int64_t>(i[1]) * L.d + k]);
-        acc = fmaf(v, c, acc);
-        sum += v;
+// ---------------------------------------------------------------------------
+// x' = x * 2^-e in fp16, one row per grouped row, with 2^e and sum_k x.  e puts
+// the row's largest magnitude in [2^14, 2^15).  Vector j of the layer (d
+// values) takes columns H j .. H j + d - 1, H = 8 (d <= 8) or 16, zeros in the
+// rest, so that the weight tiles hold centroids in whole 16-byte chunks.
+// ---------------------------------------------------------------------------
+constexpr int kPrepThreads = 256;
+
+__device__ __forceinline__ float value16(uint16_t u, int x_fp16) { return x_fp16 ? h2f(u) : bf2f(u); }
+
+__global__ void __launch_bounds__(kPrepThreads) experts_prep_kernel(
+    const uint16_t* __restrict__ x, int x_fp16, int x_rows, int64_t ldx, const int32_t* __restrict__ rows,
+    const int32_t* __restrict__ offsets, int n_experts, int kin, int d, int64_t kp, int vec, uint16_t* __restrict__ xh,
+    float* __restrict__ xe, float* __restrict__ xsum, int* __restrict__ joined, int n_joined) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  __shared__ float s_max[kPrepThreads / 32], s_sum[kPrepThreads / 32];
+  const int r = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (r == 0)
+    for (int i = tid; i < n_joined; i += kPrepThreads) joined[i] = 0;
+  bool used = false;                       // is the row in front of some group's end?
+  for (int k = tid; k <= n_experts; k += kPrepThreads) used |= __ldg(offsets + k) > r;
+  if (!__syncthreads_or(used)) return;
+  const int src = rows ? __ldg(rows + r) : r;
+  const bool live = src >= 0 && src < x_rows;
+  const uint16_t* xr = x + (live ? src : 0) * ldx;
+  float mx = 0.0f, sm = 0.0f;
+  if (live) {
+    const int whole = vec ? kin / 8 : 0;
+    for (int g = tid; g < whole; g += kPrepThreads) {
+      const uint4 q = __ldg(reinterpret_cast<const uint4*>(xr) + g);
+      const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float lo = value16(static_cast<uint16_t>(w[i] & 0xFFFFu), x_fp16);
+        const float hi = value16(static_cast<uint16_t>(w[i] >> 16), x_fp16);
+        mx = fmaxf(mx, fmaxf(fabsf(lo), fabsf(hi)));
+        sm += lo;
+        sm += hi;
       }
     }
-    const float s = L.scale ? h2f(L.scale[o]) : 1.0f, t = L.bias ? h2f(L.bias[o]) : 0.0f;
-    store_out(y, yt, r * ldy + o, s * acc + t * sum + out_bias_of(L.ob, o));
+    for (int k = 8 * whole + tid; k < kin; k += kPrepThreads) {
+      const float v = value16(__ldg(xr + k), x_fp16);
+      mx = fmaxf(mx, fabsf(v));
+      sm += v;
+    }
+  }
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) {
+    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+    sm += __shfl_xor_sync(0xffffffffu, sm, off);
+  }
+  if (lane == 0) {
+    s_max[warp] = mx;
+    s_sum[warp] = sm;
+  }
+  __syncthreads();
+  mx = sm = 0.0f;
+#pragma unroll
+  for (int w = 0; w < kPrepThreads / 32; ++w) {
+    mx = fmaxf(mx, s_max[w]);
+    sm += s_sum[w];
+  }
+  int e = 0;
+  if (mx > 0.0f && mx < INFINITY) e = max(-126, min(127, static_cast<int>(__float_as_uint(mx) >> 23) - 126 - 15));
+  const float f1 = __uint_as_float(static_cast<uint32_t>(127 - e / 2) << 23);   // 2^-e as two normal factors
+  const float f2 = __uint_as_float(static_cast<uint32_t>(127 - (e - e / 2)) << 23);
+  const int chunks = static_cast<int>(kp / 8), per = d > 8 ? 2 : 1;
+  for (int g = tid; g < chunks; g += kPrepThreads) {
+    const int first = (g / per) * d + 8 * (g % per);       // element in column 8 g
+    const int n = live ? min(min(8, d - 8 * (g % per)), kin - first) : 0;
+    float v[8];
+    if (vec && d % 8 == 0 && n == 8) {
+      const uint4 q = __ldg(reinterpret_cast<const uint4*>(xr + first));
+      const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        v[2 * i] = value16(static_cast<uint16_t>(w[i] & 0xFFFFu), x_fp16);
+        v[2 * i + 1] = value16(static_cast<uint16_t>(w[i] >> 16), x_fp16);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = i < n ? value16(__ldg(xr + first + i), x_fp16) : 0.0f;
+    }
+    uint32_t h[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      h[i] = f2h(v[2 * i] * f1 * f2) | (static_cast<uint32_t>(f2h(v[2 * i + 1] * f1 * f2)) << 16);
+    *reinterpret_cast<uint4*>(xh + r * kp + 8 * static_cast<int64_t>(g)) = make_uint4(h[0], h[1], h[2], h[3]);
+  }
+  if (tid == 0) {
+    xe[r] = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+    xsum[r] = sm;
+  }
+}
+
+// ---------------------------------------------------------------------------
+// The product.  y^T = W_e x'^T per expert: 128 rows of W are the MMA's M, up to
+// 512 rows of the group its N (two products of at most 256), so that a decoding
+// step's one row and a prompt's hundreds take the same path and W is decoded
+// once per 512 rows.
+//
+//  * Sixteen producer warps decode W: a thread owns a quarter of a row's step
+//    (64 columns), reads its index fields, gathers the centroids (small books
+//    staged in shared memory, large ones through L2) one step ahead, adds the
+//    two books' and writes the 128-byte-swizzled tile.
+//  * x' arrives by TMA in a ring of its own; one thread issues tcgen05.mma;
+//    four warps read the accumulators back and store y.
+//  * The work of all groups is one line of (expert, row tile, token tile,
+//    step), cut into equal shares, one per CTA, whatever the group sizes.  A
+//    tile that two or more CTAs share is joined through the workspace: each
+//    writes its partial sums, and the one that arrives last adds them in the
+//    order of the shares (no wait, and the same order every time).
+//  * Every wait is bounded (VQ_ERR_TIMEOUT in the status word).
+// ---------------------------------------------------------------------------
+using namespace sm100;
+
+constexpr int kRowTile = 128;
+constexpr int kATile = kRowTile * 128;            // one step of W: 64 halves a row
+constexpr int kThreads = 768;                     // warp 0: x', 1: products, 4-7: epilogue, 8-23: producers
+constexpr int kProducer0 = 256;
+constexpr int kProducers = 512;
+constexpr int kMaxA = 4, kMaxX = 8;
+constexpr int kMaxTokens = 512;
+constexpr int kMinSteps = 8;                      // least steps worth a CTA
+constexpr int kSnap = 4;                          // a share's border this near a tile's is moved there
+constexpr long long kDrain = 1LL << 26;
+
+struct Ctrl {
+  uint64_t fulla[kMaxA], emptya[kMaxA];
+  uint64_t fullx[kMaxX], emptyx[kMaxX];
+  uint64_t accf[2], acce[2];
+  uint32_t tmem;
+  int abort;
+  int last;                                       // the epilogue's CTA is the last at a joined tile
+};
+
+struct Args {
+  Experts E;
+  const int32_t* offsets;
+  int m;
+  int nkt;                  // steps of the input dimension
+  int row_tiles;
+  int tokens;               // largest token tile (multiple of 16)
+  int na, nx;               // slots of the two rings
+  int xslot;                // bytes of an x slot
+  int staged;               // bit m: book m in shared memory
+  int off_book[2];          // its first byte behind the rings
+  int off_table;            // the same of the borders' table
+  const float* xe;
+  const float* xsum;
+  void* y;
+  vq_dtype yt;
+  int64_t ldy;
+  float* part;              // [CTA][2][tokens][128] partial sums
+  int* joined;              // [CTA] arrivals at the tile that CTA starts and does not finish
+  int* status;
+  long long budget;
+};
+
+__device__ __forceinline__ uint8_t* align1024(uint8_t* p) {
+  return reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(p) + 1023) & ~uintptr_t(1023));
+}
+__device__ __forceinline__ uint32_t sw128_off(int r, int c) {
+  return static_cast<uint32_t>(r * 128 + ((c ^ (r & 7)) << 4));
+}
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ void sts128(uint32_t a, const uint4& v) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+__device__ __forceinline__ uint32_t hadd2_u32(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("add.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint4 hadd8(const uint4& a, const uint4& b) {
+  return make_uint4(hadd2_u32(a.x, b.x), hadd2_u32(a.y, b.y), hadd2_u32(a.z, b.z), hadd2_u32(a.w, b.w));
+}
+
+// True on all threads of named barrier `id` (count threads) if `ok` is on all.
+__device__ __forceinline__ bool barrier_all(int id, int count, bool ok) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.b32 q, %3, 0;\n\t"
+      "bar.red.and.pred p, %1, %2, q;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}\n"
+      : "=r"(r)
+      : "r"(id), "r"(count), "r"(static_cast<uint32_t>(ok))
+      : "memory");
+  return r != 0;
+}
+
+// The line of work.  off: group borders (clamped), first: token tiles before
+// each expert, both in shared memory.
+struct Line {
+  const int* off;
+  const int* first;
+  int experts, row_tiles, nkt, tokens;
+  int ctas;                 // CTAs with a share
+  int64_t steps;            // of all tiles
+
+  __device__ __forceinline__ int64_t border(int c) const {      // first step of CTA c's share
+    if (c <= 0) return 0;
+    if (c >= ctas) return steps;
+    const int64_t b = steps * c / ctas;
+    const int64_t tile = b / nkt;
+    const int in = static_cast<int>(b - tile * nkt);
+    if (in < kSnap) return tile * nkt;
+    if (nkt - in < kSnap) return (tile + 1) * nkt;
+    return b;
+  }
+};
+
+// One CTA's part of one tile.
+struct Part {
+  int64_t tile;
+  int expert, row0, r0, live, n;     // first W row; first grouped row, its rows, those padded to 16
+  int kt0, kt1;
+
+  __device__ __forceinline__ Part(const Line& l, int64_t at, int64_t end) {
+    tile = at / l.nkt;
+    kt0 = static_cast<int>(at - tile * l.nkt);
+    kt1 = static_cast<int>(min(static_cast<int64_t>(l.nkt), kt0 + (end - at)));
+    // the expert: the last one whose tiles start at or before this one
+    int lo = 0, hi = l.experts - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (static_cast<int64_t>(l.first[mid]) * l.row_tiles <= tile) lo = mid;
+      else hi = mid - 1;
+    }
+    expert = lo;
+    const int tt = l.first[lo + 1] - l.first[lo];
+    const int64_t in = tile - static_cast<int64_t>(l.first[lo]) * l.row_tiles;   // row tile major
+    const int rt = static_cast<int>(in / tt), j = static_cast<int>(in - static_cast<int64_t>(rt) * tt);
+    const int count = l.off[lo + 1] - l.off[lo];
+    const int per = ((count + tt - 1) / tt + 15) / 16 * 16;
+    row0 = rt * kRowTile;
+    r0 = l.off[lo] + j * per;
+    live = min(per, count - j * per);
+    n = (live + 15) / 16 * 16;
+  }
+  __device__ __forceinline__ int halves() const { return n > 256 ? 2 : 1; }
+  // rows of half h (multiples of 16, at most 256)
+  __device__ __forceinline__ int half_rows(int h) const {
+    if (n <= 256) return n;
+    const int a = (n / 2 + 15) / 16 * 16;
+    return h == 0 ? a : n - a;
+  }
+};
+
+// Index fields of a thread: VPT consecutive fields of row o of book m at step
+// kt, the thread being quarter p of the row.  Words past the stream's row (or
+// tile) read as zero: their fields belong to vectors past the last, which meet
+// zeros of x'.
+template <int LAYOUT, int VPT>
+struct Fields {
+  const uint32_t* base;     // row order: the row; tiled: the record's word in tile p / ... of step 0
+  int64_t step;             // tiled: words between steps
+  int64_t bit0;             // row order: first bit at step 0; tiled: bits into the word
+  int bits, left, tile, tiles, per;
+
+  __device__ __forceinline__ void set(const Layer& L, int m, int64_t o, int p) {
+    bits = L.b[m];
+    if constexpr (LAYOUT == VQ_IDX_TILE4) {
+      per = VPT == 2 ? 2 : 1;                                  // tiles per step
+      tile = VPT == 2 ? p >> 1 : 0;
+      const int64_t bit = (4 * o + (VPT == 2 ? 2 * (p & 1) : p)) * bits;
+      base = L.idx[m] + tile * L.rw[m] + (bit >> 5);
+      bit0 = bit & 31;
+      left = static_cast<int>(min(static_cast<int64_t>(2), L.rw[m] - (bit >> 5)));
+      step = per * L.rw[m];
+      tiles = (L.nvec + 3) / 4;
+    } else {
+      base = L.idx[m] + o * L.rw[m];
+      bit0 = static_cast<int64_t>(VPT * p) * bits;
+      step = L.rw[m];
+    }
+  }
+  __device__ __forceinline__ void load(int kt, uint32_t (&w)[2], int& sh) const {
+    w[0] = w[1] = 0u;
+    if constexpr (LAYOUT == VQ_IDX_TILE4) {
+      sh = static_cast<int>(bit0);
+      if (tile + per * kt < tiles) {
+        const uint32_t* q = base + kt * step;
+        if (left > 0) w[0] = __ldg(q);
+        if (left > 1 && sh + VPT * bits > 32) w[1] = __ldg(q + 1);
+      }
+    } else {
+      const int64_t bit = bit0 + static_cast<int64_t>(kt) * (4 * VPT * bits);
+      const int64_t at = bit >> 5;
+      sh = static_cast<int>(bit & 31);
+      if (at < step) w[0] = __ldg(base + at);
+      if (sh + VPT * bits > 32 && at + 1 < step) w[1] = __ldg(base + at + 1);
+    }
+  }
+};
+
+// Where a book is read from.
+struct Book {
+  uint32_t smem;            // staged: shared address, rows of 16 (d <= 8) or 32 bytes
+  const uint16_t* global;   // else rows of d halves
+};
+
+enum Source { kAny = 0, kStaged = 1, kLarge = 2 };   // kernels: see the dispatch
+
+// Chunk q (16 bytes) of entry i.  KIND 1: staged; 2: global, d = 8; 0: asks.
+template <int KIND, int CH>
+__device__ __forceinline__ uint4 centroid(const Book& b, bool staged, int d, uint32_t i, int q) {
+  if (KIND == 1 || (KIND == 0 && staged)) return lds128(b.smem + i * (16 * CH) + 16 * q);
+  if (KIND == 2 || (KIND == 0 && d == 8 * CH))
+    return __ldg(reinterpret_cast<const uint4*>(b.global + static_cast<size_t>(i) * (8 * CH)) + q);
+  const uint16_t* r = b.global + static_cast<size_t>(i) * d + 8 * q;
+  uint32_t w[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+  for (int e = 0; e < 8; ++e)
+    if (8 * q + e < d) w[e >> 1] |= static_cast<uint32_t>(__ldg(r + e)) << (16 * (e & 1));
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+template <int LAYOUT, int CH, int SRC>
+__global__ void __launch_bounds__(kThreads, 1)
+    gemm_experts_kernel(const __grid_constant__ CUtensorMap map64, const __grid_constant__ CUtensorMap map16,
+                        const __grid_constant__ Args g) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* base = align1024(smem_raw);
+  Ctrl* ctrl = reinterpret_cast<Ctrl*>(base);
+  uint8_t* aring = base + 1024;
+  uint8_t* xring = aring + g.na * kATile;
+  uint8_t* books = xring + g.nx * g.xslot;
+  const Layer& L0 = g.E.L;
+  const int n_experts = g.E.e;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  volatile int* abort_flag = &ctrl->abort;
+  int* s_off = reinterpret_cast<int*>(books + g.off_table);    // [experts + 1] borders
+  int* s_first = s_off + n_experts + 1;                        // [experts + 1] token tiles in front
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < g.na; ++s) {
+      mbar_init(&ctrl->fulla[s], kProducers / 32);
+      mbar_init(&ctrl->emptya[s], 1);
+    }
+    for (int s = 0; s < g.nx; ++s) {
+      mbar_init(&ctrl->fullx[s], 1);
+      mbar_init(&ctrl->emptyx[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&ctrl->accf[b], 1);
+      mbar_init(&ctrl->acce[b], 4);
+    }
+    ctrl->abort = 0;
+    fence_barrier_init();
+    tma_prefetch(&map64);
+    tma_prefetch(&map16);
+  }
+  if (warp == 1) {
+    tmem_alloc(&ctrl->tmem, kMaxTokens);
+    tmem_relinquish();
+  }
+  for (int k = threadIdx.x; k <= n_experts; k += kThreads) s_off[k] = min(g.m, max(0, __ldg(g.offsets + k)));
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 0) {                                   // ascending borders and the token tiles before each expert
+    const int per = (n_experts + 32) / 32;           // entries of a lane
+    const int k0 = min(lane * per, n_experts + 1), k1 = min(k0 + per, n_experts + 1);
+    int top = 0;
+    for (int k = k0; k < k1; ++k) top = max(top, s_off[k]);
+    int before = top;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, before, o);
+      if (lane >= o) before = max(before, v);
+    }
+    before = __shfl_up_sync(0xffffffffu, before, 1);
+    top = lane == 0 ? 0 : before;
+    for (int k = k0; k < k1; ++k) s_off[k] = top = max(top, s_off[k]);
+    __syncwarp();
+    int sum = 0;
+    for (int k = k0; k < min(k1, n_experts); ++k) sum += (s_off[k + 1] - s_off[k] + g.tokens - 1) / g.tokens;
+    int incl = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += v;
+    }
+    sum = incl - sum;
+    for (int k = k0; k < k1; ++k) {
+      s_first[k] = sum;
+      if (k < n_experts) sum += (s_off[k + 1] - s_off[k] + g.tokens - 1) / g.tokens;
+    }
+  }
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = ctrl->tmem;
+  Line line;
+  line.off = s_off;
+  line.first = s_first;
+  line.experts = n_experts;
+  line.row_tiles = g.row_tiles;
+  line.nkt = g.nkt;
+  line.tokens = g.tokens;
+  line.steps = static_cast<int64_t>(s_first[n_experts]) * g.row_tiles * g.nkt;
+  line.ctas = static_cast<int>(max(static_cast<int64_t>(1), min(static_cast<int64_t>(gridDim.x), line.steps / kMinSteps)));
+  const int cta = blockIdx.x;
+  const int64_t from = line.border(cta), to = line.border(cta + 1);
+  const int nbuf = g.tokens <= 256 ? 2 : 1;          // accumulators
+
+  if (warp == 0) {
+    if (lane == 0) {                                  // x' by TMA
+      asm volatile("griddepcontrol.wait;" ::: "memory");
+      int q = 0, qp = 0, issued = 0;
+      bool stop = false;
+      for (int64_t at = from; at < to && !stop;) {
+        const Part t(line, at, to);
+        at += t.kt1 - t.kt0;
+        for (int kt = t.kt0; kt < t.kt1 && !stop; ++kt) {
+          int row = t.r0;
+          for (int h = 0; h < t.halves(); ++h) {
+            if (!bounded_wait(&ctrl->emptyx[q], qp ^ 1, abort_flag, g.status, g.budget)) {
+              stop = true;
+              break;
+            }
+            const int n = t.half_rows(h);
+            uint8_t* dst = xring + q * g.xslot;
+            mbar_arrive_expect_tx(&ctrl->fullx[q], n * 128);
+            int i = 0;
+            for (; i + 64 <= n; i += 64) tma_load_2d(dst + i * 128, &map64, &ctrl->fullx[q], kt * 64, row + i);
+            for (; i < n; i += 16) tma_load_2d(dst + i * 128, &map16, &ctrl->fullx[q], kt * 64, row + i);
+            row += n;
+            ++issued;
+            if (++q == g.nx) {
+              q = 0;
+              qp ^= 1;
+            }
+          }
+        }
+      }
+      if (*abort_flag)                                // loads in flight land before the block ends
+        for (int i = max(0, issued - g.nx); i < issued; ++i)
+          drain_phase(&ctrl->fullx[i % g.nx], (i / g.nx) & 1, kDrain);
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {                                  // products
+      int q = 0, qp = 0, s = 0, sp = 0, it = 0;
+      bool stop = false;
+      for (int64_t at = from; at < to && !stop; ++it) {
+        const Part t(line, at, to);
+        at += t.kt1 - t.kt0;
+        const int buf = it % nbuf;
+        if (it >= nbuf && !bounded_wait(&ctrl->acce[buf], ((it / nbuf) & 1) ^ 1, abort_flag, g.status, g.budget)) break;
+        tc_fence_after();
+        for (int kt = t.kt0; kt < t.kt1 && !stop; ++kt) {
+          if (!bounded_wait(&ctrl->fulla[s], sp, abort_flag, g.status, g.budget)) {
+            stop = true;
+            break;
+          }
+          const uint32_t a = smem_addr(aring + s * kATile);
+          for (int h = 0; h < t.halves(); ++h) {
+            if (!bounded_wait(&ctrl->fullx[q], qp, abort_flag, g.status, g.budget)) {
+              stop = true;
+              break;
+            }
+            tc_fence_after();
+            const uint32_t idesc = f16_idesc(kRowTile, t.half_rows(h));
+            const uint32_t b = smem_addr(xring + q * g.xslot);
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              umma_f16(tmem + buf * 256 + h * 256, sw128_kmajor_desc(a + kk * 32), sw128_kmajor_desc(b + kk * 32), idesc,
+                       kt != t.kt0 || kk != 0);
+            umma_commit(&ctrl->emptyx[q]);
+            if (++q == g.nx) {
+              q = 0;
+              qp ^= 1;
+            }
+          }
+          if (stop) break;
+          umma_commit(&ctrl->emptya[s]);
+          if (++s == g.na) {
+            s = 0;
+            sp ^= 1;
+          }
+        }
+        if (!stop) umma_commit(&ctrl->accf[buf]);
+      }
+      if (*abort_flag) {                              // products in flight end before tensor memory is freed
+        const long long t0 = clock64();
+        while (clock64() - t0 < kDrain / 16) __nanosleep(1000);
+      }
+    }
+  } else if (warp >= 4 && warp < 8) {                 // epilogue: lane quarter warp & 3, one W row per thread
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int lq = warp & 3, r = 32 * lq + lane;
+    int it = 0;
+    for (int64_t at = from; at < to; ++it) {
+      const Part t(line, at, to);
+      const bool whole = t.kt0 == 0 && t.kt1 == g.nkt;
+      at += t.kt1 - t.kt0;
+      const int buf = it % nbuf;
+      const int o = t.row0 + r;
+      const Layer L = expert_layer(g.E, t.expert);
+      const bool live = o < L.n;
+      const float sc = live && L.scale ? h2f(__ldg(L.scale + o)) : 1.0f;
+      const float tb = live && L.bias ? h2f(__ldg(L.bias + o)) : 0.0f;
+      const float ob = live ? out_bias_of(L.ob, o) : 0.0f;
+      // the four warps go on together or not at all (they meet at barriers below)
+      if (!barrier_all(1, 128, bounded_wait(&ctrl->accf[buf], (it / nbuf) & 1, abort_flag, g.status, g.budget))) break;
+      tc_fence_after();
+      const uint32_t acc0 = tmem + buf * 256 + (static_cast<uint32_t>(32 * lq) << 16);
+      const int n0 = t.half_rows(0);
+      // columns c .. c + 15 of the tile start at tensor-memory column c, or 256 + c - n0 in the second half
+      auto column = [&](int c) { return acc0 + (c < n0 ? c : 256 + c - n0); };
+      if (whole) {
+        for (int c = 0; c < t.live; c += 16) {
+          uint32_t acc[16];
+          tmem_ld16(column(c), acc);
+          float xel = 0.0f, xsl = 0.0f;
+          if (c + (lane & 15) < t.live) {
+            xel = g.xe[t.r0 + c + (lane & 15)];
+            xsl = g.xsum[t.r0 + c + (lane & 15)];
+          }
+          tmem_wait_ld();
+          const int n = min(16, t.live - c);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const float e = __shfl_sync(0xffffffffu, xel, i), x = __shfl_sync(0xffffffffu, xsl, i);
+            if (live && i < n)
+              store_out(g.y, g.yt, static_cast<int64_t>(t.r0 + c + i) * g.ldy + o,
+                        sc * (__uint_as_float(acc[i]) * e) + tb * x + ob);
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ctrl->acce[buf]);
+        continue;
+      }
+      // a shared tile: the sums to this CTA's slot (1: it starts the tile, 0: it goes on with it)
+      const int64_t slot_size = static_cast<int64_t>(g.tokens) * kRowTile;
+      float* mine = g.part + (2 * static_cast<int64_t>(cta) + (t.kt0 == 0 ? 1 : 0)) * slot_size;
+      for (int c = 0; c < t.live; c += 16) {
+        uint32_t acc[16];
+        tmem_ld16(column(c), acc);
+        tmem_wait_ld();
+        const int n = min(16, t.live - c);
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          if (i < n) __stcg(mine + (c + i) * kRowTile + r, __uint_as_float(acc[i]));
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ctrl->acce[buf]);
+      // the CTAs of the tile: from the one whose share holds its first step to
+      // the one with its last
+      int c0 = cta, c1 = cta;
+      const int64_t begin = t.tile * g.nkt, end = begin + g.nkt;
+      while (c0 > 0 && line.border(c0) > begin) --c0;
+      while (line.border(c1 + 1) < end) ++c1;
+      __threadfence();
+      asm volatile("bar.sync 1, 128;" ::: "memory");
+      if (r == 0) {
+        int parts = 0;                                // shares that are not empty
+        for (int c = c0; c <= c1; ++c) parts += line.border(c + 1) > line.border(c) ? 1 : 0;
+        ctrl->last = atomicAdd(g.joined + c0, 1) == parts - 1;
+        __threadfence();
+      }
+      asm volatile("bar.sync 1, 128;" ::: "memory");
+      if (ctrl->last && live) {
+        for (int c = 0; c < t.live; ++c) {
+          float v = 0.0f;
+          for (int k = c0; k <= c1; ++k)
+            if (line.border(k + 1) > line.border(k))
+              v += __ldcg(g.part + (2 * static_cast<int64_t>(k) + (k == c0 ? 1 : 0)) * slot_size + c * kRowTile + r);
+          store_out(g.y, g.yt, static_cast<int64_t>(t.r0 + c) * g.ldy + o,
+                    sc * (v * g.xe[t.r0 + c]) + tb * g.xsum[t.r0 + c] + ob);
+        }
+      }
+      asm volatile("bar.sync 1, 128;" ::: "memory");  // `last` is read before the next tile sets it
+    }
+  } else if (warp >= 8) {                             // producers
+    constexpr int VPT = CH == 1 ? 2 : 1;              // vectors of a step per thread
+    const int pt = threadIdx.x - kProducer0;
+    // tiled: neighbouring threads take neighbouring rows (their records follow
+    // one another); row order: the four quarters of a row (its words do)
+    const int r = LAYOUT == VQ_IDX_TILE4 ? pt & 127 : pt >> 2;
+    const int p = LAYOUT == VQ_IDX_TILE4 ? pt >> 7 : pt & 3;
+    const bool two = L0.nb == 2;
+    const uint32_t mask0 = (1u << L0.b[0]) - 1u, mask1 = (1u << L0.b[1]) - 1u;
+    const bool st0 = g.staged & 1, st1 = (g.staged & 2) != 0;
+    Book book[2];
+    book[0].smem = smem_addr(books) + g.off_book[0];
+    book[1].smem = smem_addr(books) + g.off_book[1];
+    int staged_expert = -1, s = 0, sp = 0;
+    bool stop = false;                                // a warp that gave up still meets the others where books change
+    for (int64_t at = from; at < to;) {
+      const Part t(line, at, to);
+      at += t.kt1 - t.kt0;
+      const Layer L = expert_layer(g.E, t.expert);
+      book[0].global = L.book[0];
+      book[1].global = L.book[1];
+      Fields<LAYOUT, VPT> f0, f1;
+      const int64_t o = min(t.row0 + r, L.n - 1);     // rows past N repeat the last; they are never stored
+      f0.set(L, 0, o, p);
+      if (two) f1.set(L, 1, o, p);
+      // words of the next two steps, centroids of the next one in flight
+      uint32_t wa[2], wb[2] = {0u, 0u}, va[2], vb[2] = {0u, 0u};
+      int sa, sb = 0, ta, tb = 0;
+      f0.load(t.kt0, wa, sa);
+      if (two) f1.load(t.kt0, wb, sb);
+      if (staged_expert != t.expert && g.staged) {
+        const bool all = staged_expert < 0;           // books that the experts share are staged once
+        staged_expert = t.expert;
+        asm volatile("bar.sync 2, 512;" ::: "memory");   // nobody reads the old books any more
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+          if (!(g.staged & (1 << m)) || (!all && g.E.sb[m] == 0)) continue;
+          const uint16_t* src = L.book[m];
+          const int k = 1 << L.b[m];
+          for (int i = pt; i < k * CH; i += kProducers) {
+            const int e = i / CH, q = i % CH;
+            uint4 v;
+            if (L.d == 8 * CH) {
+              v = __ldg(reinterpret_cast<const uint4*>(src) + i);
+            } else {
+              uint32_t w[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+              for (int x = 0; x < 8; ++x)
+                if (8 * q + x < L.d)
+                  w[x >> 1] |= static_cast<uint32_t>(__ldg(src + static_cast<int64_t>(e) * L.d + 8 * q + x)) << (16 * (x & 1));
+              v = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+            sts128(book[m].smem + i * 16, v);
+          }
+        }
+        asm volatile("bar.sync 2, 512;" ::: "memory");
+      }
+      uint4 nxt[2];
+      auto gather = [&](const uint32_t (&a)[2], int sha, const uint32_t (&b)[2], int shb) {
+        const uint64_t x = ((static_cast<uint64_t>(a[1]) << 32) | a[0]) >> sha;
+        const uint64_t z = ((static_cast<uint64_t>(b[1]) << 32) | b[0]) >> shb;
+#pragma unroll
+        for (int v = 0; v < 2; ++v) {
+          const int field = CH == 1 ? v : 0, q = CH == 1 ? 0 : v;
+          const uint32_t i0 = static_cast<uint32_t>(x >> (field * L.b[0])) & mask0;
+          nxt[v] = centroid<SRC == kStaged ? 1 : (SRC == kLarge ? 2 : 0), CH>(book[0], st0, L.d, i0, q);
+          if (two) {
+            const uint32_t i1 = static_cast<uint32_t>(z >> (field * L.b[1])) & mask1;
+            nxt[v] = hadd8(nxt[v], centroid<SRC == kAny ? 0 : 1, CH>(book[1], st1, L.d, i1, q));
+          }
+        }
+      };
+      gather(wa, sa, wb, sb);
+      va[0] = va[1] = 0u;
+      ta = 0;
+      if (t.kt0 + 1 < t.kt1) {
+        f0.load(t.kt0 + 1, wa, sa);
+        if (two) f1.load(t.kt0 + 1, wb, sb);
+      }
+      if (t.kt0 + 2 < t.kt1) {
+        f0.load(t.kt0 + 2, va, ta);
+        if (two) f1.load(t.kt0 + 2, vb, tb);
+      }
+      for (int kt = t.kt0; kt < t.kt1 && !stop; ++kt) {
+        const uint4 c0 = nxt[0], c1 = nxt[1];
+        if (kt + 1 < t.kt1) {
+          gather(wa, sa, wb, sb);
+          wa[0] = va[0]; wa[1] = va[1]; sa = ta;
+          wb[0] = vb[0]; wb[1] = vb[1]; sb = tb;
+          if (kt + 3 < t.kt1) {
+            f0.load(kt + 3, va, ta);
+            if (two) f1.load(kt + 3, vb, tb);
+          }
+        }
+        if (!__all_sync(0xffffffffu, bounded_wait(&ctrl->emptya[s], sp ^ 1, abort_flag, g.status, g.budget))) {
+          stop = true;
+          break;
+        }
+        const uint32_t tile = smem_addr(aring + s * kATile);
+        sts128(tile + sw128_off(r, 2 * p), c0);
+        sts128(tile + sw128_off(r, 2 * p + 1), c1);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ctrl->fulla[s]);
+        if (++s == g.na) {
+          s = 0;
+          sp ^= 1;
+        }
+      }
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kMaxTokens);
+  }
+}
+
+// y = output bias for experts without inputs.
+__global__ void experts_bias_kernel(Experts E, const int32_t* __restrict__ offsets, int m, void* __restrict__ y,
+                                    vq_dtype yt, int64_t ldy) {
+  int last = 0;
+  for (int e = 0; e < E.e; ++e) {
+    const int r0 = max(last, min(m, max(0, offsets[e]))), r1 = max(r0, min(m, max(0, offsets[e + 1])));
+    last = r1;
+    for (int64_t i = blockIdx.x * static_cast<int64_t>(blockDim.x) + threadIdx.x;
+         i < static_cast<int64_t>(r1 - r0) * E.L.n; i += static_cast<int64_t>(gridDim.x) * blockDim.x) {
+      const int64_t r = i / E.L.n;
+      const int o = static_cast<int>(i - r * E.L.n);
+      store_out(y, yt, (r0 + r) * ldy + o, E.L.ob ? h2f(E.L.ob[e * E.so + o]) : 0.0f);
+    }
   }
 }
 
@@ -93,15 +774,143 @@ vq_status check_experts(const vq_experts_desc* d, Experts* E) {
   return VQ_OK;
 }
 
-size_t experts_bytes(const Experts& E, int m) { return 256; }
+size_t round256(size_t b) { return (b + 255) / 256 * 256; }
+
+// Shared memory and workspace of a call.
+struct Plan {
+  int nkt, row_tiles, tokens, ctas;
+  int64_t kp;
+  int na, nx, xslot, staged, off_book[2], off_table, smem;
+  size_t off_xe, off_sum, off_joined, off_xh, off_part, total;
+};
+
+// Books are staged in shared memory while the rings keep room, the token tile
+// is as large as m, 512 and the rings allow (W is decoded once per token
+// tile), and the rings share what is left: at least two slots of W, and x
+// slots for a step and a half (three of 256 rows, or two where less fits).
+bool fit(const Experts& E, int m, int staged, int tokens, Plan* p) {
+  const Layer& L = E.L;
+  const int ch = L.d > 8 ? 2 : 1;
+  int off = 0;
+  for (int b = 0; b < 2; ++b) {
+    p->off_book[b] = off;
+    if (staged & (1 << b)) off += (1 << L.b[b]) * 16 * ch;
+  }
+  p->off_table = off;
+  off += 8 * (E.e + 1);
+  const int room = device_smem_optin() - 2048 - off;
+  p->tokens = std::min((m + 15) / 16 * 16, tokens);
+  p->xslot = std::min(p->tokens, 256) * 128;
+  for (int na = kMaxA; na >= 2; --na) {
+    const int nx = std::min(kMaxX, (room - na * kATile) / p->xslot);
+    const int want = p->tokens > 256 ? 3 : (na > 2 ? 3 : 2);
+    if (room >= na * kATile && nx >= want) {
+      p->na = na;
+      p->nx = nx;
+      p->staged = staged;
+      p->smem = 2048 + na * kATile + nx * p->xslot + off;
+      return true;
+    }
+  }
+  return false;
+}
+
+Plan plan_experts(const Experts& E, int m) {
+  Plan p{};
+  const Layer& L = E.L;
+  const int per = L.d > 8 ? 4 : 8;                             // vectors of a step
+  p.nkt = (L.nvec + per - 1) / per;
+  p.kp = static_cast<int64_t>(p.nkt) * 64;
+  p.row_tiles = (L.n + kRowTile - 1) / kRowTile;
+  p.ctas = device_sm_count();
+  const int both = L.nb == 2 ? 3 : 1;
+  // staging both books comes first, then the first, then the second; a book of
+  // more than 2^13 entries never fits
+  bool done = false;
+  for (int mask : {both, 1, both & 2, 0}) {
+    bool small = true;
+    for (int b = 0; b < L.nb; ++b) small &= !(mask & (1 << b)) || L.b[b] <= 13;
+    if (!small || done) continue;
+    for (int tokens : {kMaxTokens, 256, 128})
+      if (!done && fit(E, m, mask, tokens, &p)) done = true;
+  }
+  p.off_xe = 256;
+  p.off_sum = p.off_xe + round256(static_cast<size_t>(m) * 4);
+  p.off_joined = p.off_sum + round256(static_cast<size_t>(m) * 4);
+  p.off_xh = p.off_joined + round256(static_cast<size_t>(p.ctas) * 4);
+  p.off_part = p.off_xh + round256(static_cast<size_t>(m) * p.kp * 2);
+  p.total = p.off_part + static_cast<size_t>(p.ctas) * 2 * p.tokens * kRowTile * 4;
+  return p;
+}
+
+size_t experts_bytes(const Experts& E, int m) { return E.L.kin == 0 ? 256 : plan_experts(E, m).total; }
+
+long long wait_budget() {
+  if (const char* env = std::getenv("VQ_WAIT_BUDGET")) return std::atoll(env);
+  return 4000000000LL;
+}
+
+template <int LAYOUT>
+auto pick_kernel(const Layer& L, int staged) {
+  // both books staged; a 2^16-entry book of whole 16-byte rows read through L2
+  // (a second one staged); anything else
+  if (L.d > 8) return gemm_experts_kernel<LAYOUT, 2, kAny>;
+  if (staged == (L.nb == 2 ? 3 : 1)) return gemm_experts_kernel<LAYOUT, 1, kStaged>;
+  if (L.d == 8 && staged == (L.nb == 2 ? 2 : 0)) return gemm_experts_kernel<LAYOUT, 1, kLarge>;
+  return gemm_experts_kernel<LAYOUT, 1, kAny>;
+}
 
 vq_status launch_gemm_experts(const Experts& E, const void* x, bool x_fp16, int x_rows, int64_t ldx,
                               const int32_t* rows, const int32_t* offsets, int m, void* y, vq_dtype yt, int64_t ldy,
                               void* ws, cudaStream_t stream) {
+  const Layer& L = E.L;
+  if (L.kin == 0) {
+    count_launch();
+    experts_bias_kernel<<<device_sm_count(), 256, 0, stream>>>(E, offsets, m, y, yt, ldy);
+    return cuda_status(cudaGetLastError());
+  }
+  const Plan p = plan_experts(E, m);
+  uint8_t* w = static_cast<uint8_t*>(ws);
+  uint16_t* xh = reinterpret_cast<uint16_t*>(w + p.off_xh);
+  Args g{};
+  g.E = E;
+  g.offsets = offsets;
+  g.m = m;
+  g.nkt = p.nkt;
+  g.row_tiles = p.row_tiles;
+  g.tokens = p.tokens;
+  g.na = p.na;
+  g.nx = p.nx;
+  g.xslot = p.xslot;
+  g.staged = p.staged;
+  g.off_book[0] = p.off_book[0];
+  g.off_book[1] = p.off_book[1];
+  g.off_table = p.off_table;
+  float* xe = reinterpret_cast<float*>(w + p.off_xe);
+  float* xsum = reinterpret_cast<float*>(w + p.off_sum);
+  g.xe = xe;
+  g.xsum = xsum;
+  g.y = y;
+  g.yt = yt;
+  g.ldy = ldy;
+  g.part = reinterpret_cast<float*>(w + p.off_part);
+  g.joined = reinterpret_cast<int*>(w + p.off_joined);
+  g.status = reinterpret_cast<int*>(w);
+  g.budget = wait_budget();
+  CUtensorMap map64, map16;
+  if (!make_map_f16_sw128(&map64, xh, p.kp, m, p.kp, 64) || !make_map_f16_sw128(&map16, xh, p.kp, m, p.kp, 16))
+    return VQ_ERR_CUDA;
+  const int vec = aligned(x, 16) && ldx % 8 == 0;
   count_launch();
-  gemm_experts_kernel<<<dim3((E.L.n + 127) / 128, std::min(m, 65535)), 128, 0, stream>>>(
-      E, static_cast<const uint16_t*>(x), x_fp16 ? 1 : 0, x_rows, ldx, rows, offsets, m, y, yt, ldy);
-  return cuda_status(cudaGetLastError());
+  experts_prep_kernel<<<m, kPrepThreads, 0, stream>>>(static_cast<const uint16_t*>(x), x_fp16 ? 1 : 0, x_rows, ldx, rows,
+                                                      offsets, E.e, L.kin, L.d, p.kp, vec, xh, xe, xsum, g.joined, p.ctas);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return cuda_status(e);
+  auto k = L.layout == VQ_IDX_TILE4 ? pick_kernel<VQ_IDX_TILE4>(L, p.staged) : pick_kernel<VQ_IDX_ROWS>(L, p.staged);
+  e = set_func_attr(reinterpret_cast<const void*>(k), cudaFuncAttributeMaxDynamicSharedMemorySize, p.smem);
+  if (e != cudaSuccess) return cuda_status(e);
+  count_launch();
+  return cuda_status(launch_pdl(k, dim3(p.ctas), dim3(kThreads), p.smem, stream, map64, map16, g));
 }
 
 }  // namespace

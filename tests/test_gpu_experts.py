@@ -357,6 +357,24 @@ def test_two_streams_at_once():
     assert all(torch.equal(a, b) for a, b in zip(got, want))
 
 
+@pytest.mark.parametrize("counts", [[3, 0, 2], [300, 40, 700]])
+def test_device_waits_give_up_with_a_status(monkeypatch, counts):
+    """A wait whose budget is zero gives up: the call ends, the status word
+    says so and stays set, and the next call is right."""
+    vq = _vq()
+    data, ex = _experts(LayerSpec(900, 1000, 8, (12, 8), (0.02, 0.005)), 3, "tile4", 31)
+    x, offsets = torch.randn((sum(counts), 1000), device="cuda").bfloat16(), _offsets(counts)
+    work = torch.zeros(vq.gemm_experts_workspace_size(ex, sum(counts)), dtype=torch.uint8, device="cuda")
+    monkeypatch.setenv("VQ_WAIT_BUDGET", "0")
+    vq.gemm_experts(ex, x, offsets, workspace=work)
+    torch.cuda.synchronize()
+    assert int(work[:4].view(torch.int32)) == vq.VQ_ERR_TIMEOUT
+    monkeypatch.delenv("VQ_WAIT_BUDGET")
+    y = vq.gemm_experts(ex, x, offsets, out_dtype=torch.float32, workspace=work)
+    _check(y, x, data, offsets, None, 0)
+    assert int(work[:4].view(torch.int32)) == vq.VQ_ERR_TIMEOUT
+
+
 def test_binding_checks():
     vq = _vq()
     data, ex = _experts(LayerSpec(32, 64, 8, (8,), (0.02,)), 2, "rows", 1)
