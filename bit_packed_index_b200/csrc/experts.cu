@@ -133,10 +133,14 @@ __global__ void __launch_bounds__(kPrepThreads) experts_prep_kernel(
 // step's one row and a prompt's hundreds take the same path and W is decoded
 // once per 512 rows.
 //
-//  * Sixteen producer warps decode W: a thread owns a quarter of a row's step
-//    (64 columns), reads its index fields, gathers the centroids (small books
-//    staged in shared memory, large ones through L2) one step ahead, adds the
-//    two books' and writes the 128-byte-swizzled tile.
+//  * Sixteen producer warps decode W.  They work in four groups of 128 threads,
+//    group i taking every fourth step (64 columns) from the i-th on; a thread
+//    owns one row of the tile: it reads the row's index fields of the step
+//    (loaded one turn ahead), gathers the centroids (small books staged in
+//    shared memory, large ones through L2), adds the two books' and writes the
+//    128-byte-swizzled row.  Whole steps per group keep the per-step cost (a
+//    barrier, the addresses) at a quarter of what it is when all warps share
+//    each step, and the other groups' steps hide a group's gather latency.
 //  * x' arrives by TMA in a ring of its own; one thread issues tcgen05.mma;
 //    four warps read the accumulators back and store y.
 //  * The work of all groups is one line of (expert, row tile, token tile,
@@ -153,6 +157,7 @@ constexpr int kATile = kRowTile * 128;            // one step of W: 64 halves a 
 constexpr int kThreads = 768;                     // warp 0: x', 1: products, 4-7: epilogue, 8-23: producers
 constexpr int kProducer0 = 256;
 constexpr int kProducers = 512;
+constexpr int kGroups = 4;                        // of 128 producer threads, each with its own steps
 constexpr int kMaxA = 4, kMaxX = 8;
 constexpr int kMaxTokens = 512;
 constexpr int kMinSteps = 8;                      // least steps worth a CTA
@@ -160,7 +165,8 @@ constexpr int kSnap = 4;                          // a share's border this near 
 constexpr long long kDrain = 1LL << 26;
 
 struct Ctrl {
-  uint64_t fulla[kMaxA], emptya[kMaxA];
+  uint64_t fulla[kMaxA];      // of a slot: its rows are written (tied: and its x' has arrived)
+  uint64_t donea[kGroups];    // of step % kGroups: its products are done
   uint64_t fullx[kMaxX], emptyx[kMaxX];
   uint64_t accf[2], acce[2];
   uint32_t tmem;
@@ -176,8 +182,10 @@ struct Args {
   int row_tiles;
   int tokens;               // largest token tile (multiple of 16)
   int na, nx;               // slots of the two rings
+  int tied;                 // step i's x' lies in x slot i % na and arrives on the W slot's barrier
   int xslot;                // bytes of an x slot
   int staged;               // bit m: book m in shared memory
+  int copies;               // bit m: eight copies of it
   int off_book[2];          // its first byte behind the rings
   int off_table;            // the same of the borders' table
   const float* xe;
@@ -194,12 +202,12 @@ struct Args {
 __device__ __forceinline__ uint8_t* align1024(uint8_t* p) {
   return reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(p) + 1023) & ~uintptr_t(1023));
 }
-__device__ __forceinline__ uint32_t sw128_off(int r, int c) {
-  return static_cast<uint32_t>(r * 128 + ((c ^ (r & 7)) << 4));
-}
 __device__ __forceinline__ uint4 lds128(uint32_t a) {
   uint4 v;
-  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(a)
+               : "memory");
   return v;
 }
 __device__ __forceinline__ void sts128(uint32_t a, const uint4& v) {
@@ -286,68 +294,114 @@ struct Part {
   }
 };
 
-// Index fields of a thread: VPT consecutive fields of row o of book m at step
-// kt, the thread being quarter p of the row.  Words past the stream's row (or
-// tile) read as zero: their fields belong to vectors past the last, which meet
-// zeros of x'.
-template <int LAYOUT, int VPT>
-struct Fields {
-  const uint32_t* base;     // row order: the row; tiled: the record's word in tile p / ... of step 0
-  int64_t step;             // tiled: words between steps
-  int64_t bit0;             // row order: first bit at step 0; tiled: bits into the word
-  int bits, left, tile, tiles, per;
+// The eight B-bit fields (B in 4, 8, 12, 16) of row o in a step, as the words
+// that hold them.  Row order: B consecutive bytes of the row's stream.  Tiled:
+// the row's 4B-bit records of two tiles.  Words past the stream's row, and
+// tiles past the last, read as zero: their fields belong to vectors past the
+// last, which meet zeros of x'.
+template <int LAYOUT, int B>
+struct Words {
+  static constexpr int per = LAYOUT == VQ_IDX_TILE4 ? (B == 4 ? 1 : B / 8 + (B == 12)) : B / 4;   // words of a record, of a step
+  static constexpr int count = LAYOUT == VQ_IDX_TILE4 ? 2 * per : per;
+  const uint32_t* base;
+  int64_t stride;           // words of a stream row / tile
+  int tiles, shift;
 
-  __device__ __forceinline__ void set(const Layer& L, int m, int64_t o, int p) {
-    bits = L.b[m];
+  __device__ __forceinline__ void set(const Layer& L, int m, int64_t o) {
+    stride = L.rw[m];
     if constexpr (LAYOUT == VQ_IDX_TILE4) {
-      per = VPT == 2 ? 2 : 1;                                  // tiles per step
-      tile = VPT == 2 ? p >> 1 : 0;
-      const int64_t bit = (4 * o + (VPT == 2 ? 2 * (p & 1) : p)) * bits;
-      base = L.idx[m] + tile * L.rw[m] + (bit >> 5);
-      bit0 = bit & 31;
-      left = static_cast<int>(min(static_cast<int64_t>(2), L.rw[m] - (bit >> 5)));
-      step = per * L.rw[m];
+      base = L.idx[m] + ((o * (4 * B)) >> 5);
+      shift = static_cast<int>((o * (4 * B)) & 31);
       tiles = (L.nvec + 3) / 4;
     } else {
-      base = L.idx[m] + o * L.rw[m];
-      bit0 = static_cast<int64_t>(VPT * p) * bits;
-      step = L.rw[m];
+      base = L.idx[m] + o * stride;
+      shift = 0;
     }
   }
-  __device__ __forceinline__ void load(int kt, uint32_t (&w)[2], int& sh) const {
-    w[0] = w[1] = 0u;
+  __device__ __forceinline__ void load(int kt, uint32_t (&w)[count]) const {
     if constexpr (LAYOUT == VQ_IDX_TILE4) {
-      sh = static_cast<int>(bit0);
-      if (tile + per * kt < tiles) {
-        const uint32_t* q = base + kt * step;
-        if (left > 0) w[0] = __ldg(q);
-        if (left > 1 && sh + VPT * bits > 32) w[1] = __ldg(q + 1);
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        const uint32_t* q = base + (2 * kt + t) * stride;
+        const bool in = 2 * kt + t < tiles;
+        if constexpr (B == 16) {
+          const uint2 v = in ? __ldg(reinterpret_cast<const uint2*>(q)) : make_uint2(0u, 0u);
+          w[2 * t] = v.x;
+          w[2 * t + 1] = v.y;
+        } else if constexpr (B == 12) {       // 48 bits from bit 0 or 16 of a word: inside two words of the tile
+          w[2 * t] = in ? __ldg(q) : 0u;
+          w[2 * t + 1] = in ? __ldg(q + 1) : 0u;
+        } else {
+          w[t] = in ? __ldg(q) : 0u;
+        }
       }
     } else {
-      const int64_t bit = bit0 + static_cast<int64_t>(kt) * (4 * VPT * bits);
-      const int64_t at = bit >> 5;
-      sh = static_cast<int>(bit & 31);
-      if (at < step) w[0] = __ldg(base + at);
-      if (sh + VPT * bits > 32 && at + 1 < step) w[1] = __ldg(base + at + 1);
+      const int64_t at = static_cast<int64_t>(kt) * per;
+      if (at + per <= stride) {
+        const uint32_t* q = base + at;
+        if constexpr (B == 16) {
+          const uint4 v = __ldg(reinterpret_cast<const uint4*>(q));
+          w[0] = v.x; w[1] = v.y; w[2] = v.z; w[3] = v.w;
+        } else if constexpr (B == 8) {
+          const uint2 v = __ldg(reinterpret_cast<const uint2*>(q));
+          w[0] = v.x; w[1] = v.y;
+        } else {
+#pragma unroll
+          for (int i = 0; i < per; ++i) w[i] = __ldg(q + i);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < per; ++i) w[i] = at + i < stride ? __ldg(base + at + i) : 0u;
+      }
+    }
+  }
+  // field of vector v of the step
+  __device__ __forceinline__ uint32_t field(const uint32_t (&w)[count], int v) const {
+    constexpr uint32_t mask = (1u << B) - 1u;
+    if constexpr (LAYOUT == VQ_IDX_TILE4) {
+      const int t = v >> 2, f = v & 3;
+      if constexpr (B == 16) return (w[2 * t + (f >> 1)] >> (16 * (f & 1))) & mask;
+      if constexpr (B == 8) return (w[t] >> (8 * f)) & mask;
+      if constexpr (B == 4) return (w[t] >> (shift + 4 * f)) & mask;
+      // 12: the record moved down to bit 0
+      const uint32_t lo = __funnelshift_r(w[2 * t], w[2 * t + 1], shift), hi = w[2 * t + 1] >> shift;
+      if (f == 0) return lo & mask;
+      if (f == 1) return (lo >> 12) & mask;
+      if (f == 2) return __funnelshift_r(lo, hi, 24) & mask;
+      return (hi >> 4) & mask;
+    } else {
+      const int bit = v * B;
+      const int q = bit >> 5;
+      return __funnelshift_r(w[q], q + 1 < count ? w[q + 1] : 0u, bit & 31) & mask;
     }
   }
 };
 
-// Where a book is read from.
+// Field j of row o of any width and order.
+__device__ __forceinline__ uint32_t any_field(const Layer& L, int m, int64_t o, int j) {
+  const int b = L.b[m];
+  return L.layout == VQ_IDX_ROWS ? load_field(L.idx[m] + o * L.rw[m], static_cast<int64_t>(j) * b, b)
+                                 : load_field(L.idx[m] + (j >> 2) * L.rw[m], (4 * o + (j & 3)) * b, b);
+}
+
+// Rows of x' that are loaded for n: whole boxes of 16 or 64, or one of 256.
+__host__ __device__ constexpr int loaded_rows(int n) { return n <= 48 ? n : (n > 192 ? 256 : (n + 63) / 64 * 64); }
+
+// Where a book is read from.  A staged entry takes 16 bytes a chunk (eight
+// values); a small book is kept eight times over, entry i's copies side by
+// side, so that the eight lanes of a shared-memory phase read eight different
+// bank groups whatever their indices.
 struct Book {
-  uint32_t smem;            // staged: shared address, rows of 16 (d <= 8) or 32 bytes
-  const uint16_t* global;   // else rows of d halves
+  uint32_t smem;            // shared address, with the lane's copy
+  int shift;                // log2 of an entry's bytes
+  const uint16_t* global;   // not staged: rows of d halves
 };
 
-enum Source { kAny = 0, kStaged = 1, kLarge = 2 };   // kernels: see the dispatch
-
-// Chunk q (16 bytes) of entry i.  KIND 1: staged; 2: global, d = 8; 0: asks.
-template <int KIND, int CH>
-__device__ __forceinline__ uint4 centroid(const Book& b, bool staged, int d, uint32_t i, int q) {
-  if (KIND == 1 || (KIND == 0 && staged)) return lds128(b.smem + i * (16 * CH) + 16 * q);
-  if (KIND == 2 || (KIND == 0 && d == 8 * CH))
-    return __ldg(reinterpret_cast<const uint4*>(b.global + static_cast<size_t>(i) * (8 * CH)) + q);
+// Chunk q of entry i of a book that may be staged or not, d of any size.
+__device__ __forceinline__ uint4 any_centroid(const Book& b, bool staged, int d, uint32_t i, int q) {
+  if (staged) return lds128(b.smem + (i << b.shift) + 16 * q);
   const uint16_t* r = b.global + static_cast<size_t>(i) * d + 8 * q;
+  if (d % 8 == 0) return __ldg(reinterpret_cast<const uint4*>(r));
   uint32_t w[4] = {0u, 0u, 0u, 0u};
 #pragma unroll
   for (int e = 0; e < 8; ++e)
@@ -355,9 +409,13 @@ __device__ __forceinline__ uint4 centroid(const Book& b, bool staged, int d, uin
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-template <int LAYOUT, int CH, int SRC>
+// B1 > 0: d <= 8, books of 2^B1 and 2^B2 (0: no second) entries; the second
+// staged, the first staged or (B1 = 16) read through L2 with d = 8.  B1 = 0:
+// any layer.
+template <int LAYOUT, int B1, int B2>
 __global__ void __launch_bounds__(kThreads, 1)
-    gemm_experts_kernel(const __grid_constant__ CUtensorMap map64, const __grid_constant__ CUtensorMap map16,
+    gemm_experts_kernel(const __grid_constant__ CUtensorMap map256, const __grid_constant__ CUtensorMap map64,
+                        const __grid_constant__ CUtensorMap map16,
                         const __grid_constant__ Args g) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* base = align1024(smem_raw);
@@ -367,16 +425,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* books = xring + g.nx * g.xslot;
   const Layer& L0 = g.E.L;
   const int n_experts = g.E.e;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = uniform(static_cast<int>(threadIdx.x >> 5)), lane = threadIdx.x & 31;
   volatile int* abort_flag = &ctrl->abort;
   int* s_off = reinterpret_cast<int*>(books + g.off_table);    // [experts + 1] borders
   int* s_first = s_off + n_experts + 1;                        // [experts + 1] token tiles in front
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < g.na; ++s) {
-      mbar_init(&ctrl->fulla[s], kProducers / 32);
-      mbar_init(&ctrl->emptya[s], 1);
-    }
+    for (int s = 0; s < g.na; ++s) mbar_init(&ctrl->fulla[s], kProducers / 32 / kGroups + g.tied);
+    for (int s = 0; s < kGroups; ++s) mbar_init(&ctrl->donea[s], 1);
     for (int s = 0; s < g.nx; ++s) {
       mbar_init(&ctrl->fullx[s], 1);
       mbar_init(&ctrl->emptyx[s], 1);
@@ -387,6 +443,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     ctrl->abort = 0;
     fence_barrier_init();
+    tma_prefetch(&map256);
     tma_prefetch(&map64);
     tma_prefetch(&map16);
   }
@@ -428,7 +485,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = ctrl->tmem;
+  const uint32_t tmem = uniform(ctrl->tmem);
   Line line;
   line.off = s_off;
   line.first = s_first;
@@ -442,87 +499,148 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int64_t from = line.border(cta), to = line.border(cta + 1);
   const int nbuf = g.tokens <= 256 ? 2 : 1;          // accumulators
 
-  if (warp == 0) {
-    if (lane == 0) {                                  // x' by TMA
-      asm volatile("griddepcontrol.wait;" ::: "memory");
-      int q = 0, qp = 0, issued = 0;
-      bool stop = false;
-      for (int64_t at = from; at < to && !stop;) {
-        const Part t(line, at, to);
-        at += t.kt1 - t.kt0;
-        for (int kt = t.kt0; kt < t.kt1 && !stop; ++kt) {
-          int row = t.r0;
-          for (int h = 0; h < t.halves(); ++h) {
-            if (!bounded_wait(&ctrl->emptyx[q], qp ^ 1, abort_flag, g.status, g.budget)) {
-              stop = true;
-              break;
-            }
-            const int n = t.half_rows(h);
+  // The loops of the two issuing warps are on the critical path of small tiles,
+  // so what can be worked out per tile or once is.
+  if (warp == 0) {                                    // x' by TMA
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    int q = 0, qp = 0, issued = 0;                    // x slot, its phase, loads issued
+    bool stop = false;
+    for (int64_t at = from; at < to && !stop;) {
+      const Part t(line, at, to);
+      at += t.kt1 - t.kt0;
+      const int n0 = uniform(t.half_rows(0)), n1 = uniform(t.n) - n0, r0 = uniform(t.r0);
+      const int kt1 = uniform(t.kt1);
+      for (int kt = uniform(t.kt0); kt < kt1; ++kt) {
+        int row = r0, n = n0;
+        do {
+          uint64_t* bar;
+          if (g.tied) {                               // one slot per step, free once step i - na is done
+            const int freed = issued - g.na;
+            bar = &ctrl->fulla[q];
+            stop = freed >= 0 &&
+                   !warp_wait(&ctrl->donea[freed % kGroups], (freed / kGroups) & 1, abort_flag, g.status, g.budget);
+          } else {
+            bar = &ctrl->fullx[q];
+            stop = !warp_wait(&ctrl->emptyx[q], qp ^ 1, abort_flag, g.status, g.budget);
+          }
+          if (stop) break;
+          if (elect_one()) {
             uint8_t* dst = xring + q * g.xslot;
-            mbar_arrive_expect_tx(&ctrl->fullx[q], n * 128);
-            int i = 0;
-            for (; i + 64 <= n; i += 64) tma_load_2d(dst + i * 128, &map64, &ctrl->fullx[q], kt * 64, row + i);
-            for (; i < n; i += 16) tma_load_2d(dst + i * 128, &map16, &ctrl->fullx[q], kt * 64, row + i);
-            row += n;
-            ++issued;
-            if (++q == g.nx) {
-              q = 0;
-              qp ^= 1;
+            mbar_arrive_expect_tx(bar, loaded_rows(n) * 128);
+            if (n > 192) {
+              tma_load_2d(dst, &map256, bar, kt * 64, row);
+            } else if (n > 48) {
+              for (int i = 0; i < n; i += 64) tma_load_2d(dst + i * 128, &map64, bar, kt * 64, row + i);
+            } else {
+              for (int i = 0; i < n; i += 16) tma_load_2d(dst + i * 128, &map16, bar, kt * 64, row + i);
             }
           }
-        }
+          __syncwarp();
+          ++issued;
+          if (++q == g.nx) {
+            q = 0;
+            qp ^= 1;
+          }
+          row += n;
+          n = row == r0 + n0 ? n1 : 0;
+        } while (n > 0);
+        if (stop) break;
       }
-      if (*abort_flag)                                // loads in flight land before the block ends
-        for (int i = max(0, issued - g.nx); i < issued; ++i)
-          drain_phase(&ctrl->fullx[i % g.nx], (i / g.nx) & 1, kDrain);
     }
-  } else if (warp == 1) {
-    if (lane == 0) {                                  // products
-      int q = 0, qp = 0, s = 0, sp = 0, it = 0;
-      bool stop = false;
-      for (int64_t at = from; at < to && !stop; ++it) {
-        const Part t(line, at, to);
-        at += t.kt1 - t.kt0;
-        const int buf = it % nbuf;
-        if (it >= nbuf && !bounded_wait(&ctrl->acce[buf], ((it / nbuf) & 1) ^ 1, abort_flag, g.status, g.budget)) break;
-        tc_fence_after();
-        for (int kt = t.kt0; kt < t.kt1 && !stop; ++kt) {
-          if (!bounded_wait(&ctrl->fulla[s], sp, abort_flag, g.status, g.budget)) {
+    if (*abort_flag && lane == 0)                     // loads in flight land before the block ends
+      for (int i = max(0, issued - g.nx); i < issued; ++i)
+        drain_phase(g.tied ? &ctrl->fulla[i % g.nx] : &ctrl->fullx[i % g.nx], (i / g.nx) & 1, kDrain / 16);
+  } else if (warp == 1) {                             // products
+    const uint64_t adesc0 = sw128_kmajor_desc(smem_addr(aring)), xdesc0 = sw128_kmajor_desc(smem_addr(xring));
+    const uint32_t xstep = static_cast<uint32_t>(g.xslot) >> 4;
+    int q = 0, qp = 0, s = 0, sp = 0, it = 0, step = 0;
+    bool stop = false;
+    for (int64_t at = from; at < to && !stop; ++it) {
+      const Part t(line, at, to);
+      at += t.kt1 - t.kt0;
+      const int buf = it % nbuf;
+      if (it >= nbuf && !warp_wait(&ctrl->acce[buf], ((it / nbuf) & 1) ^ 1, abort_flag, g.status, g.budget)) break;
+      tc_fence_after();
+      const uint32_t d0 = tmem + buf * 256;
+      const uint32_t id0 = uniform(f16_idesc(kRowTile, t.half_rows(0)));
+      const uint32_t id1 = uniform(t.halves() == 2 ? f16_idesc(kRowTile, t.half_rows(1)) : 0u);
+      const int kt0 = uniform(t.kt0), kt1 = uniform(t.kt1);
+      uint32_t add = 0;
+      // A barrier's test takes longer than a product of a few rows, so the next
+      // one's is under way while this step's products are issued.
+      bool ready = false;
+      if (g.tied) {
+        for (int kt = kt0; kt < kt1; ++kt, ++step) {
+          if (!ready && !warp_wait(&ctrl->fulla[s], sp, abort_flag, g.status, g.budget)) {
             stop = true;
             break;
           }
-          const uint32_t a = smem_addr(aring + s * kATile);
-          for (int h = 0; h < t.halves(); ++h) {
-            if (!bounded_wait(&ctrl->fullx[q], qp, abort_flag, g.status, g.budget)) {
-              stop = true;
-              break;
-            }
-            tc_fence_after();
-            const uint32_t idesc = f16_idesc(kRowTile, t.half_rows(h));
-            const uint32_t b = smem_addr(xring + q * g.xslot);
-#pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-              umma_f16(tmem + buf * 256 + h * 256, sw128_kmajor_desc(a + kk * 32), sw128_kmajor_desc(b + kk * 32), idesc,
-                       kt != t.kt0 || kk != 0);
-            umma_commit(&ctrl->emptyx[q]);
-            if (++q == g.nx) {
-              q = 0;
-              qp ^= 1;
-            }
-          }
-          if (stop) break;
-          umma_commit(&ctrl->emptya[s]);
+          tc_fence_after();
+          const uint64_t ad = adesc0 + static_cast<uint32_t>(s * (kATile >> 4));
+          const uint64_t bd = xdesc0 + static_cast<uint32_t>(s) * xstep;
           if (++s == g.na) {
             s = 0;
             sp ^= 1;
           }
+          const bool next = mbar_test_wait(&ctrl->fulla[s], sp);
+          if (elect_one()) {
+            umma_f16(d0, ad, bd, id0, add);
+#pragma unroll
+            for (int kk = 1; kk < 4; ++kk) umma_f16(d0, ad + 2 * kk, bd + 2 * kk, id0, 1);
+            umma_commit(&ctrl->donea[step % kGroups]);
+          }
+          ready = __all_sync(0xffffffffu, next) && kt + 1 < kt1;
+          add = 1;
         }
-        if (!stop) umma_commit(&ctrl->accf[buf]);
+      } else {
+        bool readyx = false;
+        const int halves = id1 ? 2 : 1;
+        for (int kt = kt0; kt < kt1 && !stop; ++kt, ++step) {
+          if (!ready && !warp_wait(&ctrl->fulla[s], sp, abort_flag, g.status, g.budget)) {
+            stop = true;
+            break;
+          }
+          const uint64_t ad = adesc0 + static_cast<uint32_t>(s * (kATile >> 4));
+          if (++s == g.na) {
+            s = 0;
+            sp ^= 1;
+          }
+          for (int h = 0; h < halves; ++h) {
+            if (!readyx && !warp_wait(&ctrl->fullx[q], qp, abort_flag, g.status, g.budget)) {
+              stop = true;
+              break;
+            }
+            tc_fence_after();
+            const uint64_t bd = xdesc0 + static_cast<uint32_t>(q) * xstep;
+            uint64_t* free_bar = &ctrl->emptyx[q];
+            if (++q == g.nx) {
+              q = 0;
+              qp ^= 1;
+            }
+            const bool last = h + 1 == halves;
+            const bool nextx = mbar_test_wait(&ctrl->fullx[q], qp);
+            const bool next = mbar_test_wait(&ctrl->fulla[s], sp);
+            const uint32_t d = d0 + h * 256, id = h ? id1 : id0;
+            if (elect_one()) {
+              umma_f16(d, ad, bd, id, add);
+#pragma unroll
+              for (int kk = 1; kk < 4; ++kk) umma_f16(d, ad + 2 * kk, bd + 2 * kk, id, 1);
+              umma_commit(free_bar);
+              if (last) umma_commit(&ctrl->donea[step % kGroups]);
+            }
+            const bool more = !last || kt + 1 < kt1;
+            readyx = __all_sync(0xffffffffu, nextx) && more;
+            ready = __all_sync(0xffffffffu, next) && last && more;
+          }
+          add = 1;
+        }
       }
-      if (*abort_flag) {                              // products in flight end before tensor memory is freed
-        const long long t0 = clock64();
-        while (clock64() - t0 < kDrain / 16) __nanosleep(1000);
-      }
+      if (!stop && elect_one()) umma_commit(&ctrl->accf[buf]);
+      __syncwarp();
+    }
+    if (*abort_flag) {                                // products in flight end before tensor memory is freed
+      const long long t0 = clock64();
+      while (clock64() - t0 < kDrain / 16) __nanosleep(1000);
     }
   } else if (warp >= 4 && warp < 8) {                 // epilogue: lane quarter warp & 3, one W row per thread
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -540,7 +658,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const float tb = live && L.bias ? h2f(__ldg(L.bias + o)) : 0.0f;
       const float ob = live ? out_bias_of(L.ob, o) : 0.0f;
       // the four warps go on together or not at all (they meet at barriers below)
-      if (!barrier_all(1, 128, bounded_wait(&ctrl->accf[buf], (it / nbuf) & 1, abort_flag, g.status, g.budget))) break;
+      if (!barrier_all(1, 128, warp_wait(&ctrl->accf[buf], (it / nbuf) & 1, abort_flag, g.status, g.budget))) break;
       tc_fence_after();
       const uint32_t acc0 = tmem + buf * 256 + (static_cast<uint32_t>(32 * lq) << 16);
       const int n0 = t.half_rows(0);
@@ -613,19 +731,19 @@ __global__ void __launch_bounds__(kThreads, 1)
       asm volatile("bar.sync 1, 128;" ::: "memory");  // `last` is read before the next tile sets it
     }
   } else if (warp >= 8) {                             // producers
-    constexpr int VPT = CH == 1 ? 2 : 1;              // vectors of a step per thread
     const int pt = threadIdx.x - kProducer0;
-    // tiled: neighbouring threads take neighbouring rows (their records follow
-    // one another); row order: the four quarters of a row (its words do)
-    const int r = LAYOUT == VQ_IDX_TILE4 ? pt & 127 : pt >> 2;
-    const int p = LAYOUT == VQ_IDX_TILE4 ? pt >> 7 : pt & 3;
+    const int group = pt >> 7, r = pt & 127;
     const bool two = L0.nb == 2;
-    const uint32_t mask0 = (1u << L0.b[0]) - 1u, mask1 = (1u << L0.b[1]) - 1u;
-    const bool st0 = g.staged & 1, st1 = (g.staged & 2) != 0;
+    const int ch = L0.d > 8 ? 2 : 1;                  // chunks of a vector
     Book book[2];
-    book[0].smem = smem_addr(books) + g.off_book[0];
-    book[1].smem = smem_addr(books) + g.off_book[1];
-    int staged_expert = -1, s = 0, sp = 0;
+#pragma unroll
+    for (int m = 0; m < 2; ++m) {
+      const bool copies = (g.copies >> m) & 1;
+      book[m].shift = (copies ? 7 : 4) + (ch - 1);
+      book[m].smem = smem_addr(books) + g.off_book[m] + (copies ? (lane & 7) * 16 * ch : 0);
+    }
+    int staged_expert = -1;
+    int gs = 0;                                       // steps of this CTA's earlier tiles
     bool stop = false;                                // a warp that gave up still meets the others where books change
     for (int64_t at = from; at < to;) {
       const Part t(line, at, to);
@@ -633,15 +751,21 @@ __global__ void __launch_bounds__(kThreads, 1)
       const Layer L = expert_layer(g.E, t.expert);
       book[0].global = L.book[0];
       book[1].global = L.book[1];
-      Fields<LAYOUT, VPT> f0, f1;
       const int64_t o = min(t.row0 + r, L.n - 1);     // rows past N repeat the last; they are never stored
-      f0.set(L, 0, o, p);
-      if (two) f1.set(L, 1, o, p);
-      // words of the next two steps, centroids of the next one in flight
-      uint32_t wa[2], wb[2] = {0u, 0u}, va[2], vb[2] = {0u, 0u};
-      int sa, sb = 0, ta, tb = 0;
-      f0.load(t.kt0, wa, sa);
-      if (two) f1.load(t.kt0, wb, sb);
+      int kt = t.kt0 + ((group - gs) & (kGroups - 1));   // the group's first step
+      constexpr int W1 = B1 > 0 ? Words<LAYOUT, (B1 > 0 ? B1 : 4)>::count : 1;
+      constexpr int W2 = B2 > 0 ? Words<LAYOUT, (B2 > 0 ? B2 : 4)>::count : 1;
+      Words<LAYOUT, (B1 > 0 ? B1 : 4)> f1;
+      Words<LAYOUT, (B2 > 0 ? B2 : 4)> f2;
+      uint32_t w1[W1], w2[W2];                        // words of the group's next step
+      if constexpr (B1 > 0) {
+        f1.set(L, 0, o);
+        if constexpr (B2 > 0) f2.set(L, 1, o);
+        if (kt < t.kt1) {
+          f1.load(kt, w1);
+          if constexpr (B2 > 0) f2.load(kt, w2);
+        }
+      }
       if (staged_expert != t.expert && g.staged) {
         const bool all = staged_expert < 0;           // books that the experts share are staged once
         staged_expert = t.expert;
@@ -650,12 +774,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int m = 0; m < 2; ++m) {
           if (!(g.staged & (1 << m)) || (!all && g.E.sb[m] == 0)) continue;
           const uint16_t* src = L.book[m];
-          const int k = 1 << L.b[m];
-          for (int i = pt; i < k * CH; i += kProducers) {
-            const int e = i / CH, q = i % CH;
+          const bool copies = (g.copies >> m) & 1;
+          const uint32_t dst = smem_addr(books) + g.off_book[m];
+          const int total = (ch << L.b[m]) << (copies ? 3 : 0);   // 16-byte chunks to write
+          for (int i = pt; i < total; i += kProducers) {
+            const int q = i & (ch - 1), e = copies ? i / (8 * ch) : i / ch;
             uint4 v;
-            if (L.d == 8 * CH) {
-              v = __ldg(reinterpret_cast<const uint4*>(src) + i);
+            if (L.d % 8 == 0) {
+              v = __ldg(reinterpret_cast<const uint4*>(src + static_cast<int64_t>(e) * L.d + 8 * q));
             } else {
               uint32_t w[4] = {0u, 0u, 0u, 0u};
 #pragma unroll
@@ -664,63 +790,108 @@ __global__ void __launch_bounds__(kThreads, 1)
                   w[x >> 1] |= static_cast<uint32_t>(__ldg(src + static_cast<int64_t>(e) * L.d + 8 * q + x)) << (16 * (x & 1));
               v = make_uint4(w[0], w[1], w[2], w[3]);
             }
-            sts128(book[m].smem + i * 16, v);
+            sts128(dst + i * 16, v);
           }
         }
         asm volatile("bar.sync 2, 512;" ::: "memory");
       }
-      uint4 nxt[2];
-      auto gather = [&](const uint32_t (&a)[2], int sha, const uint32_t (&b)[2], int shb) {
-        const uint64_t x = ((static_cast<uint64_t>(a[1]) << 32) | a[0]) >> sha;
-        const uint64_t z = ((static_cast<uint64_t>(b[1]) << 32) | b[0]) >> shb;
+      for (; kt < t.kt1 && !stop; kt += kGroups) {
+        // Step i writes slot i % na once step i - na is done with it.  That
+        // step's barrier is shared with step i - na - 4 alone of the earlier
+        // ones, which this group saw done before it wrote step i - 4, so the
+        // barrier's phase cannot be mistaken for an older one.
+        const int step = gs + (kt - t.kt0), freed = step - g.na;
+        const int s = step % g.na;
+        auto slot_free = [&] {
+          return freed < 0 || warp_wait(&ctrl->donea[freed % kGroups], (freed / kGroups) & 1, abort_flag, g.status, g.budget);
+        };
+        const uint32_t row = smem_addr(aring + s * kATile) + r * 128;
+        if constexpr (B1 == 16) {
+          // Straight into the tile: no registers and no lines of L1 (what is
+          // left of it beside the rings holds too few for the gathers of a
+          // step) wait for the centroids.  The other groups' steps are in flight
+          // meanwhile.
+          if (!slot_free()) {
+            stop = true;
+            break;
+          }
 #pragma unroll
-        for (int v = 0; v < 2; ++v) {
-          const int field = CH == 1 ? v : 0, q = CH == 1 ? 0 : v;
-          const uint32_t i0 = static_cast<uint32_t>(x >> (field * L.b[0])) & mask0;
-          nxt[v] = centroid<SRC == kStaged ? 1 : (SRC == kLarge ? 2 : 0), CH>(book[0], st0, L.d, i0, q);
-          if (two) {
-            const uint32_t i1 = static_cast<uint32_t>(z >> (field * L.b[1])) & mask1;
-            nxt[v] = hadd8(nxt[v], centroid<SRC == kAny ? 0 : 1, CH>(book[1], st1, L.d, i1, q));
+          for (int v = 0; v < 8; ++v)
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(row + ((v ^ (r & 7)) << 4)),
+                         "l"(reinterpret_cast<const uint4*>(book[0].global) + f1.field(w1, v))
+                         : "memory");
+          asm volatile("cp.async.commit_group;" ::: "memory");
+          uint32_t i2[8];
+          if constexpr (B2 > 0) {
+#pragma unroll
+            for (int v = 0; v < 8; ++v) i2[v] = f2.field(w2, v);
+          }
+          if (kt + kGroups < t.kt1) {
+            f1.load(kt + kGroups, w1);
+            if constexpr (B2 > 0) f2.load(kt + kGroups, w2);
+          }
+          asm volatile("cp.async.wait_group 0;" ::: "memory");
+          if constexpr (B2 > 0) {
+#pragma unroll
+            for (int v = 0; v < 8; ++v) {
+              const uint32_t a = row + ((v ^ (r & 7)) << 4);
+              sts128(a, hadd8(lds128(a), lds128(book[1].smem + (i2[v] << book[1].shift))));
+            }
+          }
+        } else if constexpr (B1 > 0) {
+          uint4 c[8];
+#pragma unroll
+          for (int v = 0; v < 8; ++v) {
+            const uint32_t i = f1.field(w1, v);
+            c[v] = lds128(book[0].smem + (i << book[0].shift));
+          }
+          if constexpr (B2 > 0) {
+#pragma unroll
+            for (int v = 0; v < 8; ++v) c[v] = hadd8(c[v], lds128(book[1].smem + (f2.field(w2, v) << book[1].shift)));
+          }
+          if (kt + kGroups < t.kt1) {
+            f1.load(kt + kGroups, w1);
+            if constexpr (B2 > 0) f2.load(kt + kGroups, w2);
+          }
+          if (!slot_free()) {
+            stop = true;
+            break;
+          }
+#pragma unroll
+          for (int v = 0; v < 8; ++v) sts128(row + ((v ^ (r & 7)) << 4), c[v]);
+        } else {
+          if (!slot_free()) {
+            stop = true;
+            break;
+          }
+          const int vectors = 8 / ch;
+          for (int v = 0; v < vectors; ++v) {
+            const int j = kt * vectors + v;
+            uint4 c[2];
+            c[0] = c[1] = make_uint4(0u, 0u, 0u, 0u);
+            if (j < L.nvec) {
+#pragma unroll
+              for (int m = 0; m < 2; ++m) {
+                if (m == 1 && !two) break;
+                const uint32_t i = any_field(L, m, o, j);
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                  if (q >= ch) break;
+                  const uint4 u = any_centroid(book[m], (g.staged >> m) & 1, L.d, i, q);
+                  c[q] = m == 0 ? u : hadd8(c[q], u);
+                }
+              }
+            }
+#pragma unroll
+            for (int q = 0; q < 2; ++q)
+              if (q < ch) sts128(row + (((v * ch + q) ^ (r & 7)) << 4), c[q]);
           }
         }
-      };
-      gather(wa, sa, wb, sb);
-      va[0] = va[1] = 0u;
-      ta = 0;
-      if (t.kt0 + 1 < t.kt1) {
-        f0.load(t.kt0 + 1, wa, sa);
-        if (two) f1.load(t.kt0 + 1, wb, sb);
-      }
-      if (t.kt0 + 2 < t.kt1) {
-        f0.load(t.kt0 + 2, va, ta);
-        if (two) f1.load(t.kt0 + 2, vb, tb);
-      }
-      for (int kt = t.kt0; kt < t.kt1 && !stop; ++kt) {
-        const uint4 c0 = nxt[0], c1 = nxt[1];
-        if (kt + 1 < t.kt1) {
-          gather(wa, sa, wb, sb);
-          wa[0] = va[0]; wa[1] = va[1]; sa = ta;
-          wb[0] = vb[0]; wb[1] = vb[1]; sb = tb;
-          if (kt + 3 < t.kt1) {
-            f0.load(kt + 3, va, ta);
-            if (two) f1.load(kt + 3, vb, tb);
-          }
-        }
-        if (!__all_sync(0xffffffffu, bounded_wait(&ctrl->emptya[s], sp ^ 1, abort_flag, g.status, g.budget))) {
-          stop = true;
-          break;
-        }
-        const uint32_t tile = smem_addr(aring + s * kATile);
-        sts128(tile + sw128_off(r, 2 * p), c0);
-        sts128(tile + sw128_off(r, 2 * p + 1), c1);
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&ctrl->fulla[s]);
-        if (++s == g.na) {
-          s = 0;
-          sp ^= 1;
-        }
       }
+      gs += t.kt1 - t.kt0;
     }
   }
   __syncwarp();
@@ -780,39 +951,43 @@ size_t round256(size_t b) { return (b + 255) / 256 * 256; }
 struct Plan {
   int nkt, row_tiles, tokens, ctas;
   int64_t kp;
-  int na, nx, xslot, staged, off_book[2], off_table, smem;
+  int na, nx, tied, xslot, staged, copies, off_book[2], off_table, smem;
   size_t off_xe, off_sum, off_joined, off_xh, off_part, total;
 };
 
-// Books are staged in shared memory while the rings keep room, the token tile
-// is as large as m, 512 and the rings allow (W is decoded once per token
-// tile), and the rings share what is left: at least two slots of W, and x
-// slots for a step and a half (three of 256 rows, or two where less fits).
-bool fit(const Experts& E, int m, int staged, int tokens, Plan* p) {
+constexpr int kMaxCopied = 8;      // log2 entries of a book that may be kept eight times (32 KB at d <= 8)
+
+// Whether books (mask `staged`, those of `copies` eight times) and rings fit for
+// token tiles of at most `tokens` rows.  Up to 256 rows every W slot has its x
+// slot, and there are at least three; above, at least two W slots and x slots
+// (256 rows) for a step and a half.
+bool fit(const Experts& E, int m, int staged, int copies, int tokens, Plan* p) {
   const Layer& L = E.L;
   const int ch = L.d > 8 ? 2 : 1;
   int off = 0;
   for (int b = 0; b < 2; ++b) {
     p->off_book[b] = off;
-    if (staged & (1 << b)) off += (1 << L.b[b]) * 16 * ch;
+    if (staged & (1 << b)) off += ((1 << L.b[b]) * 16 * ch) << ((copies >> b) & 1 ? 3 : 0);
   }
   p->off_table = off;
   off += 8 * (E.e + 1);
   const int room = device_smem_optin() - 2048 - off;
   p->tokens = std::min((m + 15) / 16 * 16, tokens);
-  p->xslot = std::min(p->tokens, 256) * 128;
-  for (int na = kMaxA; na >= 2; --na) {
-    const int nx = std::min(kMaxX, (room - na * kATile) / p->xslot);
-    const int want = p->tokens > 256 ? 3 : (na > 2 ? 3 : 2);
-    if (room >= na * kATile && nx >= want) {
-      p->na = na;
-      p->nx = nx;
-      p->staged = staged;
-      p->smem = 2048 + na * kATile + nx * p->xslot + off;
-      return true;
-    }
+  p->tied = p->tokens <= 256;
+  p->xslot = loaded_rows(std::min(p->tokens, 256)) * 128;
+  if (p->tied) {
+    p->na = p->nx = std::min(kMaxA, room / (kATile + p->xslot));
+    if (p->na < 3) return false;
+  } else {
+    p->na = kMaxA;
+    while (p->na > 2 && (room - p->na * kATile) / p->xslot < 3) --p->na;
+    p->nx = std::min(kMaxX, (room - p->na * kATile) / p->xslot);
+    if (p->nx < 3) return false;
   }
-  return false;
+  p->staged = staged;
+  p->copies = copies;
+  p->smem = 2048 + p->na * kATile + p->nx * p->xslot + off;
+  return true;
 }
 
 Plan plan_experts(const Experts& E, int m) {
@@ -823,16 +998,24 @@ Plan plan_experts(const Experts& E, int m) {
   p.kp = static_cast<int64_t>(p.nkt) * 64;
   p.row_tiles = (L.n + kRowTile - 1) / kRowTile;
   p.ctas = device_sm_count();
+  // What comes first: books in shared memory (both, the first, the second; one
+  // of more than 2^13 entries never fits), then the token tile (W is decoded once
+  // per token tile), then eight copies of small books (their lookups meet no bank
+  // conflicts).  The tile: a power of two that holds twice the rows that the
+  // experts have on average, so that few are cut, and at least 64.
+  int want = 64;
+  while (want < kMaxTokens && static_cast<int64_t>(want) * E.e < 2 * static_cast<int64_t>(m)) want *= 2;
   const int both = L.nb == 2 ? 3 : 1;
-  // staging both books comes first, then the first, then the second; a book of
-  // more than 2^13 entries never fits
+  int small = 0;
+  for (int b = 0; b < L.nb; ++b) small |= L.b[b] <= kMaxCopied ? 1 << b : 0;
   bool done = false;
   for (int mask : {both, 1, both & 2, 0}) {
-    bool small = true;
-    for (int b = 0; b < L.nb; ++b) small &= !(mask & (1 << b)) || L.b[b] <= 13;
-    if (!small || done) continue;
-    for (int tokens : {kMaxTokens, 256, 128})
-      if (!done && fit(E, m, mask, tokens, &p)) done = true;
+    bool ok = true;
+    for (int b = 0; b < L.nb; ++b) ok &= !(mask & (1 << b)) || L.b[b] <= 13;
+    if (!ok) continue;
+    for (int tokens = want; tokens >= 32; tokens /= 2)
+      for (int copies : {mask & small, mask & small & 2, 0})
+        if (!done && fit(E, m, mask, copies, tokens, &p)) done = true;
   }
   p.off_xe = 256;
   p.off_sum = p.off_xe + round256(static_cast<size_t>(m) * 4);
@@ -850,14 +1033,23 @@ long long wait_budget() {
   return 4000000000LL;
 }
 
+// The kernels with compile-time index widths: both books staged, or a first of
+// 2^16 entries (d = 8) read through L2 and the second staged.
 template <int LAYOUT>
 auto pick_kernel(const Layer& L, int staged) {
-  // both books staged; a 2^16-entry book of whole 16-byte rows read through L2
-  // (a second one staged); anything else
-  if (L.d > 8) return gemm_experts_kernel<LAYOUT, 2, kAny>;
-  if (staged == (L.nb == 2 ? 3 : 1)) return gemm_experts_kernel<LAYOUT, 1, kStaged>;
-  if (L.d == 8 && staged == (L.nb == 2 ? 2 : 0)) return gemm_experts_kernel<LAYOUT, 1, kLarge>;
-  return gemm_experts_kernel<LAYOUT, 1, kAny>;
+  const int b1 = L.b[0], b2 = L.nb == 2 ? L.b[1] : 0;
+  if (L.d <= 8 && staged == (L.nb == 2 ? 3 : 1)) {
+    if (b1 == 12 && b2 == 8) return gemm_experts_kernel<LAYOUT, 12, 8>;
+    if (b1 == 12 && b2 == 4) return gemm_experts_kernel<LAYOUT, 12, 4>;
+    if (b1 == 12 && b2 == 0) return gemm_experts_kernel<LAYOUT, 12, 0>;
+    if (b1 == 8 && b2 == 8) return gemm_experts_kernel<LAYOUT, 8, 8>;
+    if (b1 == 8 && b2 == 0) return gemm_experts_kernel<LAYOUT, 8, 0>;
+  }
+  if (L.d == 8 && b1 == 16 && staged == (L.nb == 2 ? 2 : 0)) {
+    if (b2 == 0) return gemm_experts_kernel<LAYOUT, 16, 0>;
+    if (b2 == 8) return gemm_experts_kernel<LAYOUT, 16, 8>;
+  }
+  return gemm_experts_kernel<LAYOUT, 0, 0>;
 }
 
 vq_status launch_gemm_experts(const Experts& E, const void* x, bool x_fp16, int x_rows, int64_t ldx,
@@ -881,8 +1073,10 @@ vq_status launch_gemm_experts(const Experts& E, const void* x, bool x_fp16, int 
   g.tokens = p.tokens;
   g.na = p.na;
   g.nx = p.nx;
+  g.tied = p.tied;
   g.xslot = p.xslot;
   g.staged = p.staged;
+  g.copies = p.copies;
   g.off_book[0] = p.off_book[0];
   g.off_book[1] = p.off_book[1];
   g.off_table = p.off_table;
@@ -897,8 +1091,9 @@ vq_status launch_gemm_experts(const Experts& E, const void* x, bool x_fp16, int 
   g.joined = reinterpret_cast<int*>(w + p.off_joined);
   g.status = reinterpret_cast<int*>(w);
   g.budget = wait_budget();
-  CUtensorMap map64, map16;
-  if (!make_map_f16_sw128(&map64, xh, p.kp, m, p.kp, 64) || !make_map_f16_sw128(&map16, xh, p.kp, m, p.kp, 16))
+  CUtensorMap map256, map64, map16;
+  if (!make_map_f16_sw128(&map256, xh, p.kp, m, p.kp, 256) ||
+      !make_map_f16_sw128(&map64, xh, p.kp, m, p.kp, 64) || !make_map_f16_sw128(&map16, xh, p.kp, m, p.kp, 16))
     return VQ_ERR_CUDA;
   const int vec = aligned(x, 16) && ldx % 8 == 0;
   count_launch();
@@ -910,7 +1105,7 @@ vq_status launch_gemm_experts(const Experts& E, const void* x, bool x_fp16, int 
   e = set_func_attr(reinterpret_cast<const void*>(k), cudaFuncAttributeMaxDynamicSharedMemorySize, p.smem);
   if (e != cudaSuccess) return cuda_status(e);
   count_launch();
-  return cuda_status(launch_pdl(k, dim3(p.ctas), dim3(kThreads), p.smem, stream, map64, map16, g));
+  return cuda_status(launch_pdl(k, dim3(p.ctas), dim3(kThreads), p.smem, stream, map256, map64, map16, g));
 }
 
 }  // namespace

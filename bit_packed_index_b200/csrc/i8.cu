@@ -233,7 +233,7 @@ __global__ void __launch_bounds__(kNarrowThreads) gemm_i8_narrow_kernel(const __
   NarrowCtrl* ctrl = reinterpret_cast<NarrowCtrl*>(base);
   uint8_t* stages = base + 1024;
   const int stage = kWTile + g.tn * kStepBytes;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = uniform(static_cast<int>(threadIdx.x >> 5)), lane = threadIdx.x & 31;
   const int splits = gridDim.y, split = blockIdx.y;          // the cluster spans the grid's y
   const int row0 = blockIdx.x * kRows;
   const int kt0 = split * g.kt_per_split;
@@ -262,45 +262,62 @@ __global__ void __launch_bounds__(kNarrowThreads) gemm_i8_narrow_kernel(const __
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = ctrl->tmem;
+  const uint32_t tmem = uniform(ctrl->tmem);
   pdl_wait();
 
   if (warp == 0) {
-    if (lane == 0) {
-      int issued = min(nkt, g.stages);
+    int issued = min(nkt, g.stages);
+    if (elect_one())
       for (int i = 0; i < issued; ++i)
         tma_load_2d(stages + i * stage + kWTile, &xmap, &ctrl->full[i], (kt0 + i) * kStepBytes, 0);
-      for (int i = issued; i < nkt; ++i) {
-        const int s = i % g.stages;
-        if (!bounded_wait(&ctrl->empty[s], ((i / g.stages) & 1) ^ 1, abort_flag, g.status, g.budget)) break;
+    __syncwarp();
+    int s = 0, sp = 0;
+    for (int i = issued; i < nkt; ++i) {
+      if (!warp_wait(&ctrl->empty[s], sp, abort_flag, g.status, g.budget)) break;
+      if (elect_one()) {
         mbar_arrive_expect_tx(&ctrl->full[s], stage);
         tma_load_2d(stages + s * stage, &wmap, &ctrl->full[s], (kt0 + i) * kStepBytes, row0);
         tma_load_2d(stages + s * stage + kWTile, &xmap, &ctrl->full[s], (kt0 + i) * kStepBytes, 0);
-        issued = i + 1;
       }
-      if (*abort_flag)                                       // loads in flight land before the block ends
-        for (int i = max(0, issued - g.stages); i < issued; ++i)
-          drain_phase(&ctrl->full[i % g.stages], (i / g.stages) & 1, kDrain);
+      __syncwarp();
+      issued = i + 1;
+      if (++s == g.stages) {
+        s = 0;
+        sp ^= 1;
+      }
     }
+    if (*abort_flag && lane == 0)                            // loads in flight land before the block ends
+      for (int i = max(0, issued - g.stages); i < issued; ++i)
+        drain_phase(&ctrl->full[i % g.stages], (i / g.stages) & 1, kDrain);
   } else if (warp == 1) {
-    if (lane == 0) {
-      const uint32_t idesc = i8_idesc(kRows, g.tn);
-      for (int i = 0; i < nkt; ++i) {
-        const int s = i % g.stages;
-        if (!bounded_wait(&ctrl->full[s], (i / g.stages) & 1, abort_flag, g.status, g.budget)) break;
-        tc_fence_after();
-        const uint32_t a = smem_addr(stages + s * stage);
-#pragma unroll
-        for (int kk = 0; kk < kStepBytes / 32; ++kk)
-          umma_i8(tmem, sw128_kmajor_desc(a + kk * 32), sw128_kmajor_desc(a + kWTile + kk * 32), idesc, (i | kk) != 0);
-        umma_commit(&ctrl->empty[s]);
+    const uint32_t idesc = i8_idesc(kRows, g.tn);
+    const uint64_t desc0 = sw128_kmajor_desc(smem_addr(stages));
+    int s = 0, sp = 0;
+    bool ready = false;
+    for (int i = 0; i < nkt; ++i) {
+      if (!ready && !warp_wait(&ctrl->full[s], sp, abort_flag, g.status, g.budget)) break;
+      tc_fence_after();
+      const uint64_t ad = desc0 + static_cast<uint32_t>(s * stage >> 4), bd = ad + (kWTile >> 4);
+      uint64_t* free_bar = &ctrl->empty[s];
+      if (++s == g.stages) {
+        s = 0;
+        sp ^= 1;
       }
+      const bool next = mbar_test_wait(&ctrl->full[s], sp);
+      if (elect_one()) {
+#pragma unroll
+        for (int kk = 0; kk < kStepBytes / 32; ++kk) umma_i8(tmem, ad + 2 * kk, bd + 2 * kk, idesc, (i | kk) != 0);
+        umma_commit(free_bar);
+      }
+      ready = __all_sync(0xffffffffu, next) && i + 1 < nkt;
+    }
+    if (elect_one()) {
       umma_commit(&ctrl->acc);
       drain_phase(&ctrl->acc, 0, kDrain);                    // nothing runs in tensor memory after this
     }
   } else {
     const int lq = warp & 3, r = 32 * lq + lane, o = row0 + r;
-    const bool ok = __all_sync(0xffffffffu, bounded_wait(&ctrl->acc, 0, abort_flag, g.status, g.budget));
+    const bool ok = warp_wait(&ctrl->acc, 0, abort_flag, g.status, g.budget);
     tc_fence_after();
     const uint32_t t = tmem + (static_cast<uint32_t>(32 * lq) << 16);
     if (splits == 1) {
@@ -383,7 +400,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1)
   uint8_t* stages = base + 1024;
   const int half = g.tn / 2;                                 // rows of q per CTA
   const int stage = kWTile + half * kStepBytes;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = uniform(static_cast<int>(threadIdx.x >> 5)), lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();
   const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
   const int tiles = g.tiles_n * g.tiles_m;
@@ -411,62 +428,75 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1)
   cluster_arrive();                                          // both CTAs' barriers exist
   cluster_wait();
   tc_fence_after();
-  const uint32_t tmem = ctrl->tmem;
+  const uint32_t tmem = uniform(ctrl->tmem);
   pdl_wait();
 
   if (warp == 0) {
-    if (lane == 0) {
-      int gs = 0;
-      bool stop = false;
-      for (int tile = pair; tile < tiles && !stop; tile += pairs) {
-        const int row0 = (tile / g.tiles_m) * 2 * kRows + rank * kRows;
-        const int t0 = (tile % g.tiles_m) * g.tn + rank * half;
-        for (int i = 0; i < g.num_kt; ++i, ++gs) {
-          const int s = gs % g.stages;
-          if (!bounded_wait(&ctrl->empty[s], ((gs / g.stages) & 1) ^ 1, abort_flag, g.status, g.budget)) {
-            stop = true;
-            break;
-          }
+    int s = 0, sp = 0, gs = 0;
+    bool stop = false;
+    for (int tile = pair; tile < tiles && !stop; tile += pairs) {
+      const int row0 = (tile / g.tiles_m) * 2 * kRows + rank * kRows;
+      const int t0 = (tile % g.tiles_m) * g.tn + rank * half;
+      for (int i = 0; i < g.num_kt; ++i, ++gs) {
+        if (!warp_wait(&ctrl->empty[s], sp ^ 1, abort_flag, g.status, g.budget)) {
+          stop = true;
+          break;
+        }
+        if (elect_one()) {
           const uint32_t bar = cluster_addr(&ctrl->full[s], 0);
           if (rank == 0) mbar_arrive_expect_tx(&ctrl->full[s], 2 * stage);
           tma_load_2d_pair(stages + s * stage, &wmap, bar, i * kStepBytes, row0);
           tma_load_2d_pair(stages + s * stage + kWTile, &xmap, bar, i * kStepBytes, t0);
         }
-      }
-      // the last products' arrivals on this CTA's barriers are in
-      for (int i = max(0, gs - g.stages); i < gs && !*abort_flag; ++i)
-        bounded_wait(&ctrl->empty[i % g.stages], (i / g.stages) & 1, abort_flag, g.status, g.budget);
-      if (*abort_flag) {
-        // Loads in flight land before the block ends.  Their barriers may
-        // never complete once one CTA of the pair has given up, so time does.
-        const long long t0 = clock64();
-        while (clock64() - t0 < kDrain / 16) __nanosleep(1000);
+        __syncwarp();
+        if (++s == g.stages) {
+          s = 0;
+          sp ^= 1;
+        }
       }
     }
+    // the last products' arrivals on this CTA's barriers are in
+    for (int i = max(0, gs - g.stages); i < gs && !stop; ++i)
+      stop = !warp_wait(&ctrl->empty[i % g.stages], (i / g.stages) & 1, abort_flag, g.status, g.budget);
+    if (*abort_flag) {
+      // Loads in flight land before the block ends.  Their barriers may
+      // never complete once one CTA of the pair has given up, so time does.
+      const long long t0 = clock64();
+      while (clock64() - t0 < kDrain / 16) __nanosleep(1000);
+    }
   } else if (warp == 1) {
-    if (lane == 0 && rank == 0) {
+    if (rank == 0) {
       const uint32_t idesc = i8_idesc(2 * kRows, g.tn);
-      int gs = 0, it = 0;
-      bool stop = false;
+      const uint64_t desc0 = sw128_kmajor_desc(smem_addr(stages));
+      int s = 0, sp = 0, it = 0;
+      bool stop = false, ready = false;
       for (int tile = pair; tile < tiles && !stop; tile += pairs, ++it) {
         const int buf = it & 1;
-        if (it >= 2 && !bounded_wait(&ctrl->acce[buf], ((it >> 1) & 1) ^ 1, abort_flag, g.status, g.budget)) break;
+        if (it >= 2 && !warp_wait(&ctrl->acce[buf], ((it >> 1) & 1) ^ 1, abort_flag, g.status, g.budget)) break;
         tc_fence_after();
-        for (int i = 0; i < g.num_kt; ++i, ++gs) {
-          const int s = gs % g.stages;
-          if (!bounded_wait(&ctrl->full[s], (gs / g.stages) & 1, abort_flag, g.status, g.budget)) {
+        const uint32_t d = tmem + buf * kWideTn;
+        for (int i = 0; i < g.num_kt; ++i) {
+          if (!ready && !warp_wait(&ctrl->full[s], sp, abort_flag, g.status, g.budget)) {
             stop = true;
             break;
           }
           tc_fence_after();
-          const uint32_t a = smem_addr(stages + s * stage);
+          const uint64_t ad = desc0 + static_cast<uint32_t>(s * stage >> 4), bd = ad + (kWTile >> 4);
+          uint64_t* free_bar = &ctrl->empty[s];
+          if (++s == g.stages) {
+            s = 0;
+            sp ^= 1;
+          }
+          const bool next = mbar_test_wait(&ctrl->full[s], sp);
+          if (elect_one()) {
 #pragma unroll
-          for (int kk = 0; kk < kStepBytes / 32; ++kk)
-            umma_i8_pair(tmem + buf * kWideTn, sw128_kmajor_desc(a + kk * 32), sw128_kmajor_desc(a + kWTile + kk * 32),
-                         idesc, (i | kk) != 0);
-          umma_commit_pair(&ctrl->empty[s]);
+            for (int kk = 0; kk < kStepBytes / 32; ++kk) umma_i8_pair(d, ad + 2 * kk, bd + 2 * kk, idesc, (i | kk) != 0);
+            umma_commit_pair(free_bar);
+          }
+          ready = __all_sync(0xffffffffu, next);
         }
-        if (!stop) umma_commit_pair(&ctrl->accf[buf]);
+        if (!stop && elect_one()) umma_commit_pair(&ctrl->accf[buf]);
+        __syncwarp();
       }
       if (*abort_flag) {                                     // products in flight end before tensor memory is freed
         const long long t0 = clock64();
@@ -482,7 +512,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1)
       const int t0 = (tile % g.tiles_m) * g.tn;
       const bool live = o < g.n;
       const float w = live ? __ldg(g.ws + o) : 0.0f, b = live ? out_bias_of(g.ob, o) : 0.0f;
-      if (!__all_sync(0xffffffffu, bounded_wait(&ctrl->accf[buf], (it >> 1) & 1, abort_flag, g.status, g.budget))) break;
+      if (!warp_wait(&ctrl->accf[buf], (it >> 1) & 1, abort_flag, g.status, g.budget)) break;
       tc_fence_after();
       const int cols = min(g.tn, g.m - t0);
       for (int c = 0; c < cols; c += 32) {
