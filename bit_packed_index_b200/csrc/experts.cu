@@ -718,14 +718,33 @@ __global__ void __launch_bounds__(kThreads, 1)
         __threadfence();
       }
       asm volatile("bar.sync 1, 128;" ::: "memory");
-      if (ctrl->last && live) {
-        for (int c = 0; c < t.live; ++c) {
-          float v = 0.0f;
-          for (int k = c0; k <= c1; ++k)
-            if (line.border(k + 1) > line.border(k))
-              v += __ldcg(g.part + (2 * static_cast<int64_t>(k) + (k == c0 ? 1 : 0)) * slot_size + c * kRowTile + r);
-          store_out(g.y, g.yt, static_cast<int64_t>(t.r0 + c) * g.ldy + o,
-                    sc * (v * g.xe[t.r0 + c]) + tb * g.xsum[t.r0 + c] + ob);
+      if (ctrl->last) {
+        // sixteen rows at a time, so that their loads are in flight together
+        for (int c = 0; c < t.live; c += 16) {
+          const int n = min(16, t.live - c);
+          float v[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) v[i] = 0.0f;
+          for (int k = c0; k <= c1; ++k) {
+            if (line.border(k + 1) == line.border(k)) continue;
+            const float* part = g.part + (2 * static_cast<int64_t>(k) + (k == c0 ? 1 : 0)) * slot_size + c * kRowTile + r;
+            float u[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) u[i] = i < n ? __ldcg(part + i * kRowTile) : 0.0f;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) v[i] += u[i];
+          }
+          float xel = 0.0f, xsl = 0.0f;
+          if ((lane & 15) < n) {
+            xel = g.xe[t.r0 + c + (lane & 15)];
+            xsl = g.xsum[t.r0 + c + (lane & 15)];
+          }
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const float e = __shfl_sync(0xffffffffu, xel, i), x = __shfl_sync(0xffffffffu, xsl, i);
+            if (live && i < n)
+              store_out(g.y, g.yt, static_cast<int64_t>(t.r0 + c + i) * g.ldy + o, sc * (v[i] * e) + tb * x + ob);
+          }
         }
       }
       asm volatile("bar.sync 1, 128;" ::: "memory");  // `last` is read before the next tile sets it

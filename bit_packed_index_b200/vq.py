@@ -523,7 +523,18 @@ def encode(w: torch.Tensor, codebooks: Sequence[torch.Tensor], log2k: Sequence[i
 # ---------------------------------------------------------------------------
 # Layers in 8-bit integers (include/vq_i8.h).
 # ---------------------------------------------------------------------------
-_IN16 = (torch.bfloat16, torch.float16)
+# A small call takes the GPU a few microseconds, so the checks here are kept
+# cheap: one pass over plain attributes, and a message only when one fails.
+_IN16 = {torch.bfloat16: VQ_BF16, torch.float16: VQ_FP16}
+_INT8 = {torch.int8: 0}
+_INT32 = {torch.int32: 0}
+_FLOAT32 = {torch.float32: VQ_FP32}
+
+
+def _refuse(t, name: str, want: str):
+    have = (f"{t.dtype} {tuple(t.shape)} strides {t.stride()} on {t.device}" if isinstance(t, torch.Tensor)
+            else type(t).__name__)
+    raise ValueError(f"{name} must be {want}; it is {have}")
 
 
 def _need(ok: bool, what: str):
@@ -531,59 +542,67 @@ def _need(ok: bool, what: str):
         raise ValueError(what)
 
 
-def _matrix(t: torch.Tensor, name: str, dtypes, device) -> int:
-    """Row stride of a row-major matrix on `device`."""
-    _need(t.dim() == 2 and t.dtype in dtypes, f"{name} must be a matrix of {' or '.join(map(str, dtypes))}")
-    _need(t.device == device and t.is_cuda, f"{name} must be on {device}, a CUDA device")
-    rows, cols = t.shape
-    _need(cols <= 1 or t.stride(1) == 1, f"the columns of {name} must be contiguous")
-    if rows <= 1:
-        return max(cols, 1)
-    _need(t.stride(0) >= cols, f"the rows of {name} may not overlap")
-    return t.stride(0)
+def _matrix(t: torch.Tensor, name: str, types, index: int, cols: int = -1) -> int:
+    """Row stride of a row-major matrix of one of `types` on CUDA device `index`."""
+    shape = t.shape
+    if len(shape) == 2 and t.dtype in types and index >= 0 and t.get_device() == index and cols in (-1, shape[1]):
+        rows, n = shape
+        if n <= 1 or t.stride(1) == 1:
+            if rows <= 1:
+                return n or 1
+            ld = t.stride(0)
+            if ld >= n:
+                return ld
+    _refuse(t, name, f"a row-major matrix{'' if cols < 0 else f' of {cols} columns'} of "
+                     f"{' or '.join(map(str, types))} on {f'cuda:{index}' if index >= 0 else 'a CUDA device'}, "
+                     "its rows apart")
 
 
-def _vector(t: torch.Tensor, name: str, dtype, n: int, device):
-    _need(t.dim() == 1 and t.dtype == dtype and t.shape[0] == n and t.is_contiguous(),
-          f"{name} must be a contiguous vector of {n} {dtype}")
-    _need(t.device == device, f"{name} must be on {device}")
+def _vector(t: torch.Tensor, name: str, dtype, n: int, index: int):
+    if (len(t.shape) != 1 or t.dtype != dtype or t.shape[0] != n or t.get_device() != index
+            or (n > 1 and t.stride(0) != 1)):
+        _refuse(t, name, f"a contiguous vector of {n} {dtype} on cuda:{index}")
 
 
-def _output(out, rows: int, cols: int, dtype, device):
+def _output(out, rows: int, cols: int, dtype, like: torch.Tensor, index: int):
     if out is None:
-        _need(dtype in _DTYPE, f"unsupported output type {dtype}")
-        out = torch.empty((rows, cols), dtype=dtype, device=device)
-        return out, max(cols, 1)
-    ld = _matrix(out, "out", tuple(_DTYPE), device)
-    _need(tuple(out.shape) == (rows, cols), f"out must be {rows} x {cols}")
+        if dtype not in _DTYPE:
+            raise ValueError(f"unsupported output type {dtype}")
+        return like.new_empty((rows, cols), dtype=dtype), cols or 1
+    ld = _matrix(out, "out", _DTYPE, index, cols)
+    if out.shape[0] != rows:
+        _refuse(out, "out", f"{rows} x {cols}")
     return out, ld
 
 
-def _scratch(nbytes: int, device, given: Optional[torch.Tensor]):
-    """The workspace of a call whose status word the caller clears: pointer, size, owner."""
+def _scratch(nbytes: int, like: torch.Tensor, index: int, given: Optional[torch.Tensor]):
+    """Pointer, size and owner of a call's workspace (the caller's holds a
+    status word that the caller clears; see include/vq_i8.h)."""
     if given is not None:
-        _need(given.device == device and given.is_contiguous(), f"workspace must be contiguous, on {device}")
+        if given.get_device() != index or not given.is_contiguous():
+            _refuse(given, "workspace", f"contiguous, on cuda:{index}")
         return given.data_ptr(), given.numel() * given.element_size(), given
     if nbytes == 0:
         return 0, 0, None
-    t = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    t = like.new_empty(nbytes, dtype=torch.uint8)
     return t.data_ptr(), nbytes, t
 
 
-class _On:
-    """Make `device` current for a call if it is not."""
-    __slots__ = ("ctx",)
+_functions = {}
 
-    def __init__(self, device):
-        self.ctx = None if torch.cuda.current_device() == device.index else torch.cuda.device(device)
 
-    def __enter__(self):
-        if self.ctx is not None:
-            self.ctx.__enter__()
-
-    def __exit__(self, *exc):
-        if self.ctx is not None:
-            self.ctx.__exit__(*exc)
+def _run(name: str, index: int, *args):
+    """lib().<name>(*args, the current stream of device `index`) with that device current."""
+    fn = _functions.get(name)
+    if fn is None:
+        fn = _functions[name] = getattr(lib(), name)
+    if torch._C._cuda_getDevice() == index:
+        status = fn(*args, torch._C._cuda_getCurrentRawStream(index))
+    else:
+        with torch.cuda.device(index):
+            status = fn(*args, torch._C._cuda_getCurrentRawStream(index))
+    if status != VQ_OK:
+        _check(name, status)
 
 
 class Int8Layer:
@@ -593,13 +612,14 @@ class Int8Layer:
     float16 or bfloat16 matrix."""
 
     def __init__(self, weight: torch.Tensor, scale: torch.Tensor, out_bias: Optional[torch.Tensor] = None):
-        ld = _matrix(weight, "weight", (torch.int8,), weight.device)
+        self.device, self.index = weight.device, weight.get_device()
+        ld = _matrix(weight, "weight", _INT8, self.index)
         n, k = weight.shape
-        _vector(scale, "scale", torch.float32, n, weight.device)
+        _vector(scale, "scale", torch.float32, n, self.index)
         if out_bias is not None:
-            _vector(out_bias, "out_bias", torch.float16, n, weight.device)
+            _vector(out_bias, "out_bias", torch.float16, n, self.index)
         self.weight, self.scale, self.out_bias = weight, scale, out_bias
-        self.out_features, self.in_features, self.device = n, k, weight.device
+        self.out_features, self.in_features = n, k
         d = _I8Desc()
         d.out_features, d.in_features = n, k
         d.w, d.ldw = weight.data_ptr(), ld if n > 1 else -(-max(k, 1) // 16) * 16
@@ -607,7 +627,7 @@ class Int8Layer:
         d.out_bias = None if out_bias is None else out_bias.data_ptr()
         self._desc = d
         self._ref = C.addressof(d)
-        self._need = {}
+        self._sizes = {}
 
     @classmethod
     def quantise(cls, w: torch.Tensor, out_bias: Optional[torch.Tensor] = None) -> "Int8Layer":
@@ -619,11 +639,13 @@ class Int8Layer:
         return self.weight.shape[0] * (self.weight.shape[1] + 4 + (0 if self.out_bias is None else 2))
 
     def _bytes(self, fn: str, m: int) -> int:
-        """Workspace bytes of vq_<fn>_i8 for m rows."""
-        n = C.c_size_t(0)
-        name = f"vq_{fn}_i8_workspace_size"
-        _check(name, getattr(lib(), name)(self._ref, m, C.byref(n)))
-        return n.value
+        """Workspace bytes of vq_<fn>_i8 for m rows (a function of the sizes alone, so kept)."""
+        n = self._sizes.get((fn, m))
+        if n is None:
+            size, name = C.c_size_t(0), f"vq_{fn}_i8_workspace_size"
+            _check(name, getattr(lib(), name)(self._ref, m, C.byref(size)))
+            n = self._sizes[(fn, m)] = size.value
+        return n
 
 
 def gemm_i8_workspace_size(layer: Int8Layer, m: int) -> int:
@@ -638,57 +660,52 @@ def quant_i8(x: torch.Tensor, out: Optional[torch.Tensor] = None, scale: Optiona
     """(q, scale): the rows of x (bf16 or fp16 [m][n]) as int8 with one float32
     scale each (vq_quant_i8).  A new q has rows padded to 16 bytes, as gemm_i8
     and Int8Layer want them."""
-    dev = x.device
-    ldx = _matrix(x, "x", _IN16, dev)
+    index = x.get_device()
+    ldx = _matrix(x, "x", _IN16, index)
     m, n = x.shape
     if out is None:
-        ldq = -(-max(n, 1) // 16) * 16
-        out = torch.empty((m, ldq), dtype=torch.int8, device=dev)
+        ldq = -(-(n or 1) // 16) * 16
+        out = x.new_empty((m, ldq), dtype=torch.int8)
         if ldq != n:
             out = out[:, :n]
     else:
-        ldq = _matrix(out, "out", (torch.int8,), dev)
-        _need(out.shape == x.shape, "out must have x's shape")
+        ldq = _matrix(out, "out", _INT8, index, n)
+        if out.shape[0] != m:
+            _refuse(out, "out", f"{m} x {n}")
     if scale is None:
-        scale = torch.empty(m, dtype=torch.float32, device=dev)
+        scale = x.new_empty(m, dtype=torch.float32)
     else:
-        _vector(scale, "scale", torch.float32, m, dev)
-    with _On(dev):
-        _check("vq_quant_i8", lib().vq_quant_i8(x.data_ptr(), _DTYPE[x.dtype], m, n, ldx, out.data_ptr(), ldq,
-                                                scale.data_ptr(), _stream(dev)))
+        _vector(scale, "scale", torch.float32, m, index)
+    _run("vq_quant_i8", index, x.data_ptr(), _DTYPE[x.dtype], m, n, ldx, out.data_ptr(), ldq, scale.data_ptr())
     return out, scale
 
 
 def gemm_i8(layer: Int8Layer, q: torch.Tensor, q_scale: torch.Tensor, out_dtype=torch.bfloat16,
             out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
     """y [m][N] = (q . W^T) * scale * q_scale + bias for rows that quant_i8 made (vq_gemm_i8)."""
-    dev = layer.device
-    ldq = _matrix(q, "q", (torch.int8,), dev)
-    m, k = q.shape
-    _need(k == layer.in_features, f"q must have {layer.in_features} columns")
+    index = layer.index
+    ldq = _matrix(q, "q", _INT8, index, layer.in_features)
+    m = q.shape[0]
     if m <= 1:
         ldq = -(-ldq // 16) * 16
-    _vector(q_scale, "q_scale", torch.float32, m, dev)
-    out, ldy = _output(out, m, layer.out_features, out_dtype, dev)
-    with _On(dev):
-        ws, n, keep = _scratch(layer._bytes("gemm", m), dev, workspace)
-        _check("vq_gemm_i8", lib().vq_gemm_i8(layer._ref, q.data_ptr(), ldq, q_scale.data_ptr(), m, out.data_ptr(),
-                                              _DTYPE[out.dtype], ldy, ws, n, _stream(dev)))
+    _vector(q_scale, "q_scale", torch.float32, m, index)
+    out, ldy = _output(out, m, layer.out_features, out_dtype, q, index)
+    ws, n, keep = _scratch(layer._bytes("gemm", m), q, index, workspace)
+    _run("vq_gemm_i8", index, layer._ref, q.data_ptr(), ldq, q_scale.data_ptr(), m, out.data_ptr(), _DTYPE[out.dtype],
+         ldy, ws, n)
     return out
 
 
 def linear_i8(layer: Int8Layer, x: torch.Tensor, out_dtype=torch.bfloat16, out: Optional[torch.Tensor] = None,
               workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
     """y [m][N] of bf16 or fp16 activations x [m][Kin]: quant_i8 and gemm_i8 in one call (vq_linear_i8)."""
-    dev = layer.device
-    ldx = _matrix(x, "x", _IN16, dev)
-    m, k = x.shape
-    _need(k == layer.in_features, f"x must have {layer.in_features} columns")
-    out, ldy = _output(out, m, layer.out_features, out_dtype, dev)
-    with _On(dev):
-        ws, n, keep = _scratch(layer._bytes("linear", m), dev, workspace)
-        _check("vq_linear_i8", lib().vq_linear_i8(layer._ref, x.data_ptr(), _DTYPE[x.dtype], m, ldx, out.data_ptr(),
-                                                  _DTYPE[out.dtype], ldy, ws, n, _stream(dev)))
+    index = layer.index
+    ldx = _matrix(x, "x", _IN16, index, layer.in_features)
+    m = x.shape[0]
+    out, ldy = _output(out, m, layer.out_features, out_dtype, x, index)
+    ws, n, keep = _scratch(layer._bytes("linear", m), x, index, workspace)
+    _run("vq_linear_i8", index, layer._ref, x.data_ptr(), _DTYPE[x.dtype], m, ldx, out.data_ptr(), _DTYPE[out.dtype],
+         ldy, ws, n)
     return out
 
 
@@ -743,11 +760,12 @@ class Experts:
             setattr(D, name + "_stride", t.stride(0) if t.shape[0] > 1 else 0)
         D.n_experts = e
         self.n_experts, self.out_features, self.in_features, self.vec_dim = e, out_features, in_features, vec_dim
-        self.log2k, self.layout, self.device = [int(b) for b in log2k], layout, dev
+        self.log2k, self.layout, self.device, self.index = [int(b) for b in log2k], layout, dev, idx[0].get_device()
         self.idx, self.codebooks = list(idx), list(codebooks)
         self.scale, self.bias, self.out_bias = scale, bias, out_bias
         self._desc = D
         self._ref = C.addressof(D)
+        self._sizes = {}
 
     @classmethod
     def from_layers(cls, layers: Sequence[Layer]) -> "Experts":
@@ -785,32 +803,34 @@ def group_rows(ids: torch.Tensor, n_experts: int, offsets: Optional[torch.Tensor
                rows: Optional[torch.Tensor] = None, pos: Optional[torch.Tensor] = None):
     """(offsets [E+1], rows [T * top_k], pos [T][top_k]) of the picks ids (int32
     [T][top_k]) in the order of their experts (vq_group_rows)."""
-    dev = ids.device
-    ld = _matrix(ids, "ids", (torch.int32,), dev)
+    index = ids.get_device()
+    ld = _matrix(ids, "ids", _INT32, index)
     t, k = ids.shape
     if offsets is None:
-        offsets = torch.empty(max(n_experts, 0) + 1, dtype=torch.int32, device=dev)
+        offsets = ids.new_empty(max(n_experts, 0) + 1)
     else:
-        _vector(offsets, "offsets", torch.int32, n_experts + 1, dev)
+        _vector(offsets, "offsets", torch.int32, n_experts + 1, index)
     if rows is None:
-        rows = torch.empty(t * k, dtype=torch.int32, device=dev)
+        rows = ids.new_empty(t * k)
     else:
-        _vector(rows, "rows", torch.int32, t * k, dev)
+        _vector(rows, "rows", torch.int32, t * k, index)
     if pos is None:
-        pos = torch.empty((t, k), dtype=torch.int32, device=dev)
-    else:
-        _need(pos.dtype == torch.int32 and pos.device == dev and pos.shape == ids.shape and pos.is_contiguous(),
-              "pos must be contiguous int32 of ids' shape")
-    with _On(dev):
-        _check("vq_group_rows", lib().vq_group_rows(ids.data_ptr(), t, k, ld, n_experts, offsets.data_ptr(),
-                                                    rows.data_ptr(), pos.data_ptr(), _stream(dev)))
+        pos = ids.new_empty((t, k))
+    elif pos.dtype != torch.int32 or pos.get_device() != index or pos.shape != ids.shape or not pos.is_contiguous():
+        _refuse(pos, "pos", "contiguous int32 of ids' shape")
+    _run("vq_group_rows", index, ids.data_ptr(), t, k, ld, n_experts, offsets.data_ptr(), rows.data_ptr(),
+         pos.data_ptr())
     return offsets, rows, pos
 
 
 def gemm_experts_workspace_size(experts: Experts, m: int) -> int:
-    n = C.c_size_t(0)
-    _check("vq_gemm_experts_workspace_size", lib().vq_gemm_experts_workspace_size(experts._ref, m, C.byref(n)))
-    return n.value
+    n = experts._sizes.get(m)                 # a function of the sizes alone, so kept
+    if n is None:
+        size = C.c_size_t(0)
+        _check("vq_gemm_experts_workspace_size",
+               lib().vq_gemm_experts_workspace_size(experts._ref, m, C.byref(size)))
+        n = experts._sizes[m] = size.value
+    return n
 
 
 def gemm_experts(experts: Experts, x: torch.Tensor, offsets: torch.Tensor, rows: Optional[torch.Tensor] = None,
@@ -820,39 +840,37 @@ def gemm_experts(experts: Experts, x: torch.Tensor, offsets: torch.Tensor, rows:
     rows of x with expert e (vq_gemm_experts).  Grouped row r reads x[rows[r]],
     or x[r] without ``rows``; m is the length of ``rows``, else of x.  Rows
     behind the last group are not written."""
-    dev = experts.device
-    ldx = _matrix(x, "x", _IN16, dev)
-    _need(x.shape[1] == experts.in_features, f"x must have {experts.in_features} columns")
-    _vector(offsets, "offsets", torch.int32, experts.n_experts + 1, dev)
-    m = x.shape[0]
+    index = experts.index
+    ldx = _matrix(x, "x", _IN16, index, experts.in_features)
+    _vector(offsets, "offsets", torch.int32, experts.n_experts + 1, index)
+    m = x_rows = x.shape[0]
+    rows_ptr = None
     if rows is not None:
-        _need(rows.dim() == 1, "rows must be a vector")
-        m = rows.shape[0]
-        _vector(rows, "rows", torch.int32, m, dev)
-    out, ldy = _output(out, m, experts.out_features, out_dtype, dev)
-    with _On(dev):
-        ws, n, keep = _scratch(gemm_experts_workspace_size(experts, m), dev, workspace)
-        _check("vq_gemm_experts", lib().vq_gemm_experts(
-            experts._ref, x.data_ptr(), _DTYPE[x.dtype], x.shape[0], ldx, None if rows is None else rows.data_ptr(),
-            offsets.data_ptr(), m, out.data_ptr(), _DTYPE[out.dtype], ldy, ws, n, _stream(dev)))
+        _vector(rows, "rows", torch.int32, rows.numel(), index)
+        m, rows_ptr = rows.shape[0], rows.data_ptr()
+    out, ldy = _output(out, m, experts.out_features, out_dtype, x, index)
+    ws, n, keep = _scratch(gemm_experts_workspace_size(experts, m), x, index, workspace)
+    _run("vq_gemm_experts", index, experts._ref, x.data_ptr(), _DTYPE[x.dtype], x_rows, ldx, rows_ptr,
+         offsets.data_ptr(), m, out.data_ptr(), _DTYPE[out.dtype], ldy, ws, n)
     return out
 
 
 def combine_rows(z: torch.Tensor, pos: torch.Tensor, weight: torch.Tensor, out_dtype=torch.bfloat16,
                  out: Optional[torch.Tensor] = None) -> torch.Tensor:
     """y [T][n] = sum_j weight[t][j] z[pos[t][j]] over a token's picks (vq_combine_rows)."""
-    dev = z.device
-    ldz = _matrix(z, "z", tuple(_DTYPE), dev)
-    _need(pos.dim() == 2 and pos.dtype == torch.int32 and pos.device == dev and pos.is_contiguous(),
-          f"pos must be a contiguous int32 matrix on {dev}")
+    index = z.get_device()
+    ldz = _matrix(z, "z", _DTYPE, index)
+    z_rows, n = z.shape
+    _matrix(pos, "pos", _INT32, index)
     t, k = pos.shape
-    ldw = _matrix(weight, "weight", (torch.float32,), dev)
-    _need(weight.shape == pos.shape, "weight must have pos's shape")
-    out, ldy = _output(out, t, z.shape[1], out_dtype, dev)
-    with _On(dev):
-        _check("vq_combine_rows", lib().vq_combine_rows(
-            z.data_ptr(), _DTYPE[z.dtype], z.shape[0], z.shape[1], ldz, pos.data_ptr(), weight.data_ptr(), ldw, t, k,
-            out.data_ptr(), _DTYPE[out.dtype], ldy, _stream(dev)))
+    if not pos.is_contiguous():
+        _refuse(pos, "pos", "contiguous")
+    ldw = _matrix(weight, "weight", _FLOAT32, index, k)
+    if weight.shape[0] != t:
+        _refuse(weight, "weight", f"{t} x {k}")
+    out, ldy = _output(out, t, n, out_dtype, z, index)
+    _run("vq_combine_rows", index, z.data_ptr(), _DTYPE[z.dtype], z_rows, n, ldz, pos.data_ptr(), weight.data_ptr(),
+         ldw, t, k, out.data_ptr(), _DTYPE[out.dtype], ldy)
     return out
 
 
