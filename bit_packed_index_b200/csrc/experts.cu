@@ -159,7 +159,7 @@ constexpr int kProducer0 = 256;
 constexpr int kProducers = 512;
 constexpr int kGroups = 4;                        // of 128 producer threads, each with its own steps
 constexpr int kMaxA = 4, kMaxX = 8;
-constexpr int kMaxTokens = 512;
+constexpr int kTmemCols = 512;
 constexpr int kMinSteps = 8;                      // least steps worth a CTA
 constexpr int kSnap = 4;                          // a share's border this near a tile's is moved there
 constexpr long long kDrain = 1LL << 26;
@@ -242,6 +242,7 @@ struct Line {
   const int* off;
   const int* first;
   int experts, row_tiles, nkt, tokens;
+  int acc;                  // rows of an accumulator: a tile of more takes two
   int ctas;                 // CTAs with a share
   int64_t steps;            // of all tiles
 
@@ -262,8 +263,10 @@ struct Part {
   int64_t tile;
   int expert, row0, r0, live, n;     // first W row; first grouped row, its rows, those padded to 16
   int kt0, kt1;
+  int acc;
 
   __device__ __forceinline__ Part(const Line& l, int64_t at, int64_t end) {
+    acc = l.acc;
     tile = at / l.nkt;
     kt0 = static_cast<int>(at - tile * l.nkt);
     kt1 = static_cast<int>(min(static_cast<int64_t>(l.nkt), kt0 + (end - at)));
@@ -285,10 +288,10 @@ struct Part {
     live = min(per, count - j * per);
     n = (live + 15) / 16 * 16;
   }
-  __device__ __forceinline__ int halves() const { return n > 256 ? 2 : 1; }
-  // rows of half h (multiples of 16, at most 256)
+  __device__ __forceinline__ int halves() const { return n > acc ? 2 : 1; }
+  // rows of half h (multiples of 16, at most acc)
   __device__ __forceinline__ int half_rows(int h) const {
-    if (n <= 256) return n;
+    if (n <= acc) return n;
     const int a = (n / 2 + 15) / 16 * 16;
     return h == 0 ? a : n - a;
   }
@@ -409,6 +412,15 @@ __device__ __forceinline__ uint4 any_centroid(const Book& b, bool staged, int d,
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
+// W tiles whose rows pass through registers anyway (books in shared memory) lie
+// in tensor memory: a step is 32 columns, and neither the producers' stores nor
+// the products' reads of W take shared memory's cycles from the lookups, which
+// bound the kernel.  Those that cp.async fills (2^16 books) and those of the
+// general kernel lie in shared memory.  Tensor memory holds two accumulators of
+// acc_rows() rows and, in the first case, four steps of W.
+__host__ __device__ constexpr bool w_in_tmem(int b1) { return b1 > 0 && b1 < 16; }
+__host__ __device__ constexpr int acc_rows(bool in_tmem) { return in_tmem ? 192 : 256; }
+
 // B1 > 0: d <= 8, books of 2^B1 and 2^B2 (0: no second) entries; the second
 // staged, the first staged or (B1 = 16) read through L2 with d = 8.  B1 = 0:
 // any layer.
@@ -418,10 +430,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const __grid_constant__ CUtensorMap map16,
                         const __grid_constant__ Args g) {
   extern __shared__ uint8_t smem_raw[];
+  constexpr bool kInTmem = w_in_tmem(B1);
+  constexpr int kAcc = acc_rows(kInTmem);
   uint8_t* base = align1024(smem_raw);
   Ctrl* ctrl = reinterpret_cast<Ctrl*>(base);
   uint8_t* aring = base + 1024;
-  uint8_t* xring = aring + g.na * kATile;
+  uint8_t* xring = aring + (kInTmem ? 0 : g.na * kATile);
   uint8_t* books = xring + g.nx * g.xslot;
   const Layer& L0 = g.E.L;
   const int n_experts = g.E.e;
@@ -448,7 +462,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tma_prefetch(&map16);
   }
   if (warp == 1) {
-    tmem_alloc(&ctrl->tmem, kMaxTokens);
+    tmem_alloc(&ctrl->tmem, kTmemCols);
     tmem_relinquish();
   }
   for (int k = threadIdx.x; k <= n_experts; k += kThreads) s_off[k] = min(g.m, max(0, __ldg(g.offsets + k)));
@@ -493,11 +507,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   line.row_tiles = g.row_tiles;
   line.nkt = g.nkt;
   line.tokens = g.tokens;
+  line.acc = kAcc;
   line.steps = static_cast<int64_t>(s_first[n_experts]) * g.row_tiles * g.nkt;
   line.ctas = static_cast<int>(max(static_cast<int64_t>(1), min(static_cast<int64_t>(gridDim.x), line.steps / kMinSteps)));
   const int cta = blockIdx.x;
   const int64_t from = line.border(cta), to = line.border(cta + 1);
-  const int nbuf = g.tokens <= 256 ? 2 : 1;          // accumulators
+  const int nbuf = g.tokens <= kAcc ? 2 : 1;         // accumulators in turn
+  const uint32_t tmem_a = tmem + 2 * kAcc;           // W steps of 32 columns
 
   // The loops of the two issuing warps are on the critical path of small tiles,
   // so what can be worked out per tile or once is.
@@ -553,6 +569,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp == 1) {                             // products
     const uint64_t adesc0 = sw128_kmajor_desc(smem_addr(aring)), xdesc0 = sw128_kmajor_desc(smem_addr(xring));
     const uint32_t xstep = static_cast<uint32_t>(g.xslot) >> 4;
+    // the four products of a step, W from tensor or shared memory
+    auto step_products = [](uint32_t d, uint32_t at_, uint64_t ad, uint64_t bd, uint32_t id, uint32_t add) {
+#pragma unroll
+      for (int kk = 0; kk < 4; ++kk) {
+        if constexpr (kInTmem) umma_f16_ta(d, at_ + 8 * kk, bd + 2 * kk, id, kk ? 1u : add);
+        else umma_f16(d, ad + 2 * kk, bd + 2 * kk, id, kk ? 1u : add);
+      }
+    };
     int q = 0, qp = 0, s = 0, sp = 0, it = 0, step = 0;
     bool stop = false;
     for (int64_t at = from; at < to && !stop; ++it) {
@@ -561,7 +585,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int buf = it % nbuf;
       if (it >= nbuf && !warp_wait(&ctrl->acce[buf], ((it / nbuf) & 1) ^ 1, abort_flag, g.status, g.budget)) break;
       tc_fence_after();
-      const uint32_t d0 = tmem + buf * 256;
+      const uint32_t d0 = tmem + buf * kAcc;
       const uint32_t id0 = uniform(f16_idesc(kRowTile, t.half_rows(0)));
       const uint32_t id1 = uniform(t.halves() == 2 ? f16_idesc(kRowTile, t.half_rows(1)) : 0u);
       const int kt0 = uniform(t.kt0), kt1 = uniform(t.kt1);
@@ -577,6 +601,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           tc_fence_after();
           const uint64_t ad = adesc0 + static_cast<uint32_t>(s * (kATile >> 4));
+          const uint32_t at_ = tmem_a + 32 * s;
           const uint64_t bd = xdesc0 + static_cast<uint32_t>(s) * xstep;
           if (++s == g.na) {
             s = 0;
@@ -584,9 +609,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           const bool next = mbar_test_wait(&ctrl->fulla[s], sp);
           if (elect_one()) {
-            umma_f16(d0, ad, bd, id0, add);
-#pragma unroll
-            for (int kk = 1; kk < 4; ++kk) umma_f16(d0, ad + 2 * kk, bd + 2 * kk, id0, 1);
+            step_products(d0, at_, ad, bd, id0, add);
             umma_commit(&ctrl->donea[step % kGroups]);
           }
           ready = __all_sync(0xffffffffu, next) && kt + 1 < kt1;
@@ -601,6 +624,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             break;
           }
           const uint64_t ad = adesc0 + static_cast<uint32_t>(s * (kATile >> 4));
+          const uint32_t at_ = tmem_a + 32 * s;
           if (++s == g.na) {
             s = 0;
             sp ^= 1;
@@ -620,11 +644,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             const bool last = h + 1 == halves;
             const bool nextx = mbar_test_wait(&ctrl->fullx[q], qp);
             const bool next = mbar_test_wait(&ctrl->fulla[s], sp);
-            const uint32_t d = d0 + h * 256, id = h ? id1 : id0;
+            const uint32_t d = d0 + h * kAcc, id = h ? id1 : id0;
             if (elect_one()) {
-              umma_f16(d, ad, bd, id, add);
-#pragma unroll
-              for (int kk = 1; kk < 4; ++kk) umma_f16(d, ad + 2 * kk, bd + 2 * kk, id, 1);
+              step_products(d, at_, ad, bd, id, add);
               umma_commit(free_bar);
               if (last) umma_commit(&ctrl->donea[step % kGroups]);
             }
@@ -660,10 +682,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       // the four warps go on together or not at all (they meet at barriers below)
       if (!barrier_all(1, 128, warp_wait(&ctrl->accf[buf], (it / nbuf) & 1, abort_flag, g.status, g.budget))) break;
       tc_fence_after();
-      const uint32_t acc0 = tmem + buf * 256 + (static_cast<uint32_t>(32 * lq) << 16);
+      const uint32_t acc0 = tmem + buf * kAcc + (static_cast<uint32_t>(32 * lq) << 16);
       const int n0 = t.half_rows(0);
-      // columns c .. c + 15 of the tile start at tensor-memory column c, or 256 + c - n0 in the second half
-      auto column = [&](int c) { return acc0 + (c < n0 ? c : 256 + c - n0); };
+      // rows c .. c + 15 of the tile start at tensor-memory column c, or kAcc + c - n0 in the second half
+      auto column = [&](int c) { return acc0 + (c < n0 ? c : kAcc + c - n0); };
       if (whole) {
         for (int c = 0; c < t.live; c += 16) {
           uint32_t acc[16];
@@ -876,8 +898,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             stop = true;
             break;
           }
-#pragma unroll
-          for (int v = 0; v < 8; ++v) sts128(row + ((v ^ (r & 7)) << 4), c[v]);
+          tc_fence_after();
+          tmem_st32(tmem_a + 32 * s + (static_cast<uint32_t>(32 * (warp & 3)) << 16), c);
+          tmem_wait_st();
+          tc_fence_before();
         } else {
           if (!slot_free()) {
             stop = true;
@@ -906,7 +930,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (q < ch) sts128(row + (((v * ch + q) ^ (r & 7)) << 4), c[q]);
           }
         }
-        fence_proxy_async_smem();
+        if constexpr (!kInTmem) fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&ctrl->fulla[s]);
       }
@@ -918,7 +942,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc(tmem, kMaxTokens);
+    tmem_dealloc(tmem, kTmemCols);
   }
 }
 
@@ -976,10 +1000,25 @@ struct Plan {
 
 constexpr int kMaxCopied = 8;      // log2 entries of a book that may be kept eight times (32 KB at d <= 8)
 
+// The kernel that serves a layer with the books of mask `staged` in shared
+// memory: its compile-time index widths (0, 0: the general one).
+struct Widths {
+  int b1, b2;
+};
+Widths widths_of(const Layer& L, int staged) {
+  const int b1 = L.b[0], b2 = L.nb == 2 ? L.b[1] : 0;
+  if (L.d <= 8 && staged == (L.nb == 2 ? 3 : 1)) {
+    if (b1 == 12 && (b2 == 8 || b2 == 4 || b2 == 0)) return {b1, b2};
+    if (b1 == 8 && (b2 == 8 || b2 == 0)) return {b1, b2};
+  }
+  if (L.d == 8 && b1 == 16 && staged == (L.nb == 2 ? 2 : 0) && (b2 == 0 || b2 == 8)) return {b1, b2};
+  return {0, 0};
+}
+
 // Whether books (mask `staged`, those of `copies` eight times) and rings fit for
-// token tiles of at most `tokens` rows.  Up to 256 rows every W slot has its x
-// slot, and there are at least three; above, at least two W slots and x slots
-// (256 rows) for a step and a half.
+// token tiles of at most `tokens` rows.  A tile of one accumulator has an x slot
+// per W slot, at least three of each; a tile of two has at least two W slots and
+// x slots for a step and a half.
 bool fit(const Experts& E, int m, int staged, int copies, int tokens, Plan* p) {
   const Layer& L = E.L;
   const int ch = L.d > 8 ? 2 : 1;
@@ -991,21 +1030,23 @@ bool fit(const Experts& E, int m, int staged, int copies, int tokens, Plan* p) {
   p->off_table = off;
   off += 8 * (E.e + 1);
   const int room = device_smem_optin() - 2048 - off;
+  const bool in_tmem = w_in_tmem(widths_of(L, staged).b1);
+  const int acc = acc_rows(in_tmem), atile = in_tmem ? 0 : kATile;
   p->tokens = std::min((m + 15) / 16 * 16, tokens);
-  p->tied = p->tokens <= 256;
-  p->xslot = loaded_rows(std::min(p->tokens, 256)) * 128;
+  p->tied = p->tokens <= acc;
+  p->xslot = loaded_rows(std::min(p->tokens, acc)) * 128;
   if (p->tied) {
-    p->na = p->nx = std::min(kMaxA, room / (kATile + p->xslot));
+    p->na = p->nx = std::min(kMaxA, room / (atile + p->xslot));
     if (p->na < 3) return false;
   } else {
     p->na = kMaxA;
-    while (p->na > 2 && (room - p->na * kATile) / p->xslot < 3) --p->na;
-    p->nx = std::min(kMaxX, (room - p->na * kATile) / p->xslot);
+    while (p->na > 2 && (room - p->na * atile) / p->xslot < 3) --p->na;
+    p->nx = std::min(kMaxX, (room - p->na * atile) / p->xslot);
     if (p->nx < 3) return false;
   }
   p->staged = staged;
   p->copies = copies;
-  p->smem = 2048 + p->na * kATile + p->nx * p->xslot + off;
+  p->smem = 2048 + p->na * atile + p->nx * p->xslot + off;
   return true;
 }
 
@@ -1020,10 +1061,8 @@ Plan plan_experts(const Experts& E, int m) {
   // What comes first: books in shared memory (both, the first, the second; one
   // of more than 2^13 entries never fits), then the token tile (W is decoded once
   // per token tile), then eight copies of small books (their lookups meet no bank
-  // conflicts).  The tile: a power of two that holds twice the rows that the
-  // experts have on average, so that few are cut, and at least 64.
-  int want = 64;
-  while (want < kMaxTokens && static_cast<int64_t>(want) * E.e < 2 * static_cast<int64_t>(m)) want *= 2;
+  // conflicts).  The tile: the smallest of 64, 128, one and two accumulators that
+  // holds twice the rows that the experts have on average, so that few are cut.
   const int both = L.nb == 2 ? 3 : 1;
   int small = 0;
   for (int b = 0; b < L.nb; ++b) small |= L.b[b] <= kMaxCopied ? 1 << b : 0;
@@ -1032,9 +1071,13 @@ Plan plan_experts(const Experts& E, int m) {
     bool ok = true;
     for (int b = 0; b < L.nb; ++b) ok &= !(mask & (1 << b)) || L.b[b] <= 13;
     if (!ok) continue;
-    for (int tokens = want; tokens >= 32; tokens /= 2)
+    const int acc = acc_rows(w_in_tmem(widths_of(L, mask).b1));
+    const int sizes[5] = {2 * acc, acc, 128, 64, 32};
+    int first = 3;
+    while (first > 0 && static_cast<int64_t>(sizes[first]) * E.e < 2 * static_cast<int64_t>(m)) --first;
+    for (int i = first; i < 5; ++i)
       for (int copies : {mask & small, mask & small & 2, 0})
-        if (!done && fit(E, m, mask, copies, tokens, &p)) done = true;
+        if (!done && fit(E, m, mask, copies, sizes[i], &p)) done = true;
   }
   p.off_xe = 256;
   p.off_sum = p.off_xe + round256(static_cast<size_t>(m) * 4);
@@ -1052,22 +1095,16 @@ long long wait_budget() {
   return 4000000000LL;
 }
 
-// The kernels with compile-time index widths: both books staged, or a first of
-// 2^16 entries (d = 8) read through L2 and the second staged.
 template <int LAYOUT>
 auto pick_kernel(const Layer& L, int staged) {
-  const int b1 = L.b[0], b2 = L.nb == 2 ? L.b[1] : 0;
-  if (L.d <= 8 && staged == (L.nb == 2 ? 3 : 1)) {
-    if (b1 == 12 && b2 == 8) return gemm_experts_kernel<LAYOUT, 12, 8>;
-    if (b1 == 12 && b2 == 4) return gemm_experts_kernel<LAYOUT, 12, 4>;
-    if (b1 == 12 && b2 == 0) return gemm_experts_kernel<LAYOUT, 12, 0>;
-    if (b1 == 8 && b2 == 8) return gemm_experts_kernel<LAYOUT, 8, 8>;
-    if (b1 == 8 && b2 == 0) return gemm_experts_kernel<LAYOUT, 8, 0>;
-  }
-  if (L.d == 8 && b1 == 16 && staged == (L.nb == 2 ? 2 : 0)) {
-    if (b2 == 0) return gemm_experts_kernel<LAYOUT, 16, 0>;
-    if (b2 == 8) return gemm_experts_kernel<LAYOUT, 16, 8>;
-  }
+  const Widths w = widths_of(L, staged);
+  if (w.b1 == 12 && w.b2 == 8) return gemm_experts_kernel<LAYOUT, 12, 8>;
+  if (w.b1 == 12 && w.b2 == 4) return gemm_experts_kernel<LAYOUT, 12, 4>;
+  if (w.b1 == 12) return gemm_experts_kernel<LAYOUT, 12, 0>;
+  if (w.b1 == 8 && w.b2 == 8) return gemm_experts_kernel<LAYOUT, 8, 8>;
+  if (w.b1 == 8) return gemm_experts_kernel<LAYOUT, 8, 0>;
+  if (w.b1 == 16 && w.b2 == 8) return gemm_experts_kernel<LAYOUT, 16, 8>;
+  if (w.b1 == 16) return gemm_experts_kernel<LAYOUT, 16, 0>;
   return gemm_experts_kernel<LAYOUT, 0, 0>;
 }
 
