@@ -165,7 +165,7 @@ constexpr int kSnap = 4;                          // a share's border this near 
 constexpr long long kDrain = 1LL << 26;
 
 struct Ctrl {
-  uint64_t fulla[kMaxA];      // of a slot: its rows are written (tied: and its x' has arrived)
+  uint64_t fulla[kMaxA];      // of a slot: its rows are written
   uint64_t donea[kGroups];    // of step % kGroups: its products are done
   uint64_t fullx[kMaxX], emptyx[kMaxX];
   uint64_t accf[2], acce[2];
@@ -182,7 +182,7 @@ struct Args {
   int row_tiles;
   int tokens;               // largest token tile (multiple of 16)
   int na, nx;               // slots of the two rings
-  int tied;                 // step i's x' lies in x slot i % na and arrives on the W slot's barrier
+  int xk;                   // steps of an x slot
   int xslot;                // bytes of an x slot
   int staged;               // bit m: book m in shared memory
   int copies;               // bit m: eight copies of it
@@ -387,8 +387,14 @@ __device__ __forceinline__ uint32_t any_field(const Layer& L, int m, int64_t o, 
                                  : load_field(L.idx[m] + (j >> 2) * L.rw[m], (4 * o + (j & 3)) * b, b);
 }
 
-// Rows of x' that are loaded for n: whole boxes of 16 or 64, or one of 256.
-__host__ __device__ constexpr int loaded_rows(int n) { return n <= 48 ? n : (n > 192 ? 256 : (n + 63) / 64 * 64); }
+// x' comes in boxes of kBoxes rows by xk steps, one box for a tile's half: a
+// load's issue takes its thread longer than most boxes take to arrive.
+constexpr int kBoxes = 5;
+__host__ __device__ constexpr int box_rows(int i, int acc) { return i < 4 ? 16 << i : acc; }
+__host__ __device__ constexpr int box_of(int n) { return n <= 16 ? 0 : n <= 32 ? 1 : n <= 64 ? 2 : n <= 128 ? 3 : 4; }
+struct Maps {
+  CUtensorMap m[kBoxes];
+};
 
 // Where a book is read from.  A staged entry takes 16 bytes a chunk (eight
 // values); a small book is kept eight times over, entry i's copies side by
@@ -426,8 +432,7 @@ __host__ __device__ constexpr int acc_rows(bool in_tmem) { return in_tmem ? 192 
 // any layer.
 template <int LAYOUT, int B1, int B2>
 __global__ void __launch_bounds__(kThreads, 1)
-    gemm_experts_kernel(const __grid_constant__ CUtensorMap map256, const __grid_constant__ CUtensorMap map64,
-                        const __grid_constant__ CUtensorMap map16,
+    gemm_experts_kernel(const __grid_constant__ Maps maps,
                         const __grid_constant__ Args g) {
   extern __shared__ uint8_t smem_raw[];
   constexpr bool kInTmem = w_in_tmem(B1);
@@ -445,7 +450,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   int* s_first = s_off + n_experts + 1;                        // [experts + 1] token tiles in front
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < g.na; ++s) mbar_init(&ctrl->fulla[s], kProducers / 32 / kGroups + g.tied);
+    for (int s = 0; s < g.na; ++s) mbar_init(&ctrl->fulla[s], kProducers / 32 / kGroups);
     for (int s = 0; s < kGroups; ++s) mbar_init(&ctrl->donea[s], 1);
     for (int s = 0; s < g.nx; ++s) {
       mbar_init(&ctrl->fullx[s], 1);
@@ -457,9 +462,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     ctrl->abort = 0;
     fence_barrier_init();
-    tma_prefetch(&map256);
-    tma_prefetch(&map64);
-    tma_prefetch(&map16);
   }
   if (warp == 1) {
     tmem_alloc(&ctrl->tmem, kTmemCols);
@@ -525,31 +527,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       const Part t(line, at, to);
       at += t.kt1 - t.kt0;
       const int n0 = uniform(t.half_rows(0)), n1 = uniform(t.n) - n0, r0 = uniform(t.r0);
-      const int kt1 = uniform(t.kt1);
-      for (int kt = uniform(t.kt0); kt < kt1; ++kt) {
-        int row = r0, n = n0;
-        do {
-          uint64_t* bar;
-          if (g.tied) {                               // one slot per step, free once step i - na is done
-            const int freed = issued - g.na;
-            bar = &ctrl->fulla[q];
-            stop = freed >= 0 &&
-                   !warp_wait(&ctrl->donea[freed % kGroups], (freed / kGroups) & 1, abort_flag, g.status, g.budget);
-          } else {
-            bar = &ctrl->fullx[q];
-            stop = !warp_wait(&ctrl->emptyx[q], qp ^ 1, abort_flag, g.status, g.budget);
+      const int kt1 = uniform(t.kt1), b0 = box_of(n0);
+      for (int kt = uniform(t.kt0); kt < kt1 && !stop; kt += g.xk) {
+        int row = r0, box = b0;
+        for (;;) {
+          if (!warp_wait(&ctrl->emptyx[q], qp ^ 1, abort_flag, g.status, g.budget)) {
+            stop = true;
+            break;
           }
-          if (stop) break;
           if (elect_one()) {
-            uint8_t* dst = xring + q * g.xslot;
-            mbar_arrive_expect_tx(bar, loaded_rows(n) * 128);
-            if (n > 192) {
-              tma_load_2d(dst, &map256, bar, kt * 64, row);
-            } else if (n > 48) {
-              for (int i = 0; i < n; i += 64) tma_load_2d(dst + i * 128, &map64, bar, kt * 64, row + i);
-            } else {
-              for (int i = 0; i < n; i += 16) tma_load_2d(dst + i * 128, &map16, bar, kt * 64, row + i);
-            }
+            mbar_arrive_expect_tx(&ctrl->fullx[q], g.xk * box_rows(box, kAcc) * 128);
+            tma_load_3d(xring + q * g.xslot, &maps.m[box], &ctrl->fullx[q], 0, row, kt);
           }
           __syncwarp();
           ++issued;
@@ -557,15 +545,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             q = 0;
             qp ^= 1;
           }
-          row += n;
-          n = row == r0 + n0 ? n1 : 0;
-        } while (n > 0);
-        if (stop) break;
+          if (n1 == 0 || row != r0) break;
+          row += n0;
+          box = box_of(n1);
+        }
       }
     }
     if (*abort_flag && lane == 0)                     // loads in flight land before the block ends
       for (int i = max(0, issued - g.nx); i < issued; ++i)
-        drain_phase(g.tied ? &ctrl->fulla[i % g.nx] : &ctrl->fullx[i % g.nx], (i / g.nx) & 1, kDrain / 16);
+        drain_phase(&ctrl->fullx[i % g.nx], (i / g.nx) & 1, kDrain / 16);
   } else if (warp == 1) {                             // products
     const uint64_t adesc0 = sw128_kmajor_desc(smem_addr(aring)), xdesc0 = sw128_kmajor_desc(smem_addr(xring));
     const uint32_t xstep = static_cast<uint32_t>(g.xslot) >> 4;
@@ -592,9 +580,19 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t add = 0;
       // A barrier's test takes longer than a product of a few rows, so the next
       // one's is under way while this step's products are issued.
-      bool ready = false;
-      if (g.tied) {
+      bool ready = false, readyx = false;
+      if (id1 == 0) {
+        const uint32_t kstep = uniform(static_cast<uint32_t>(box_rows(box_of(t.n), kAcc))) * (128 >> 4);
+        int kk = 0;                                   // step of the x slot
+        uint64_t bd = 0;
         for (int kt = kt0; kt < kt1; ++kt, ++step) {
+          if (kk == 0) {
+            if (!readyx && !warp_wait(&ctrl->fullx[q], qp, abort_flag, g.status, g.budget)) {
+              stop = true;
+              break;
+            }
+            bd = xdesc0 + static_cast<uint32_t>(q) * xstep;
+          }
           if (!ready && !warp_wait(&ctrl->fulla[s], sp, abort_flag, g.status, g.budget)) {
             stop = true;
             break;
@@ -602,22 +600,34 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc_fence_after();
           const uint64_t ad = adesc0 + static_cast<uint32_t>(s * (kATile >> 4));
           const uint32_t at_ = tmem_a + 32 * s;
-          const uint64_t bd = xdesc0 + static_cast<uint32_t>(s) * xstep;
           if (++s == g.na) {
             s = 0;
             sp ^= 1;
           }
-          const bool next = mbar_test_wait(&ctrl->fulla[s], sp);
+          const bool next = mbar_test_wait(&ctrl->fulla[s], sp), more = kt + 1 < kt1;
+          const bool spent = ++kk == g.xk || !more;   // the x slot's last step
+          uint64_t* free_bar = &ctrl->emptyx[q];
+          bool nextx = false;
+          if (spent) {
+            kk = 0;
+            if (++q == g.nx) {
+              q = 0;
+              qp ^= 1;
+            }
+            nextx = mbar_test_wait(&ctrl->fullx[q], qp);
+          }
           if (elect_one()) {
             step_products(d0, at_, ad, bd, id0, add);
             umma_commit(&ctrl->donea[step % kGroups]);
+            if (spent) umma_commit(free_bar);
           }
-          ready = __all_sync(0xffffffffu, next) && kt + 1 < kt1;
+          bd += kstep;
+          ready = __all_sync(0xffffffffu, next) && more;
+          if (spent) readyx = __all_sync(0xffffffffu, nextx) && more;
           add = 1;
         }
       } else {
-        bool readyx = false;
-        const int halves = id1 ? 2 : 1;
+        const int halves = 2;
         for (int kt = kt0; kt < kt1 && !stop; ++kt, ++step) {
           if (!ready && !warp_wait(&ctrl->fulla[s], sp, abort_flag, g.status, g.budget)) {
             stop = true;
@@ -994,7 +1004,7 @@ size_t round256(size_t b) { return (b + 255) / 256 * 256; }
 struct Plan {
   int nkt, row_tiles, tokens, ctas;
   int64_t kp;
-  int na, nx, tied, xslot, staged, copies, off_book[2], off_table, smem;
+  int na, nx, xk, xslot, staged, copies, off_book[2], off_table, smem;
   size_t off_xe, off_sum, off_joined, off_xh, off_part, total;
 };
 
@@ -1016,9 +1026,8 @@ Widths widths_of(const Layer& L, int staged) {
 }
 
 // Whether books (mask `staged`, those of `copies` eight times) and rings fit for
-// token tiles of at most `tokens` rows.  A tile of one accumulator has an x slot
-// per W slot, at least three of each; a tile of two has at least two W slots and
-// x slots for a step and a half.
+// token tiles of at most `tokens` rows: at least two W slots, and x slots of
+// several steps, two at least, or of one step (of a half), three at least.
 bool fit(const Experts& E, int m, int staged, int copies, int tokens, Plan* p) {
   const Layer& L = E.L;
   const int ch = L.d > 8 ? 2 : 1;
@@ -1033,17 +1042,20 @@ bool fit(const Experts& E, int m, int staged, int copies, int tokens, Plan* p) {
   const bool in_tmem = w_in_tmem(widths_of(L, staged).b1);
   const int acc = acc_rows(in_tmem), atile = in_tmem ? 0 : kATile;
   p->tokens = std::min((m + 15) / 16 * 16, tokens);
-  p->tied = p->tokens <= acc;
-  p->xslot = loaded_rows(std::min(p->tokens, acc)) * 128;
-  if (p->tied) {
-    p->na = p->nx = std::min(kMaxA, room / (atile + p->xslot));
-    if (p->na < 3) return false;
-  } else {
+  const int slot = box_rows(box_of(std::min(p->tokens, acc)), acc) * 128;      // bytes of a step of x'
+  if (p->tokens <= acc) {
     p->na = kMaxA;
-    while (p->na > 2 && (room - p->na * atile) / p->xslot < 3) --p->na;
-    p->nx = std::min(kMaxX, (room - p->na * atile) / p->xslot);
+    for (p->xk = 4; p->xk > 1 && (room - p->na * atile) / (slot * p->xk) < 2; p->xk /= 2) {}
+    p->nx = std::min(kMaxX, (room - p->na * atile) / (slot * p->xk));
+    if (p->nx < (p->xk > 1 ? 2 : 3)) return false;
+  } else {
+    p->xk = 1;
+    p->na = kMaxA;
+    while (p->na > 2 && (room - p->na * atile) / slot < 3) --p->na;
+    p->nx = std::min(kMaxX, (room - p->na * atile) / slot);
     if (p->nx < 3) return false;
   }
+  p->xslot = slot * p->xk;
   p->staged = staged;
   p->copies = copies;
   p->smem = 2048 + p->na * atile + p->nx * p->xslot + off;
@@ -1129,7 +1141,7 @@ vq_status launch_gemm_experts(const Experts& E, const void* x, bool x_fp16, int 
   g.tokens = p.tokens;
   g.na = p.na;
   g.nx = p.nx;
-  g.tied = p.tied;
+  g.xk = p.xk;
   g.xslot = p.xslot;
   g.staged = p.staged;
   g.copies = p.copies;
@@ -1147,10 +1159,10 @@ vq_status launch_gemm_experts(const Experts& E, const void* x, bool x_fp16, int 
   g.joined = reinterpret_cast<int*>(w + p.off_joined);
   g.status = reinterpret_cast<int*>(w);
   g.budget = wait_budget();
-  CUtensorMap map256, map64, map16;
-  if (!make_map_f16_sw128(&map256, xh, p.kp, m, p.kp, 256) ||
-      !make_map_f16_sw128(&map64, xh, p.kp, m, p.kp, 64) || !make_map_f16_sw128(&map16, xh, p.kp, m, p.kp, 16))
-    return VQ_ERR_CUDA;
+  Maps maps;
+  const int acc = acc_rows(w_in_tmem(widths_of(L, p.staged).b1));
+  for (int i = 0; i < kBoxes; ++i)
+    if (!make_map_f16_steps(&maps.m[i], xh, p.nkt, m, p.kp, box_rows(i, acc), p.xk)) return VQ_ERR_CUDA;
   const int vec = aligned(x, 16) && ldx % 8 == 0;
   count_launch();
   experts_prep_kernel<<<m, kPrepThreads, 0, stream>>>(static_cast<const uint16_t*>(x), x_fp16 ? 1 : 0, x_rows, ldx, rows,
@@ -1161,7 +1173,7 @@ vq_status launch_gemm_experts(const Experts& E, const void* x, bool x_fp16, int 
   e = set_func_attr(reinterpret_cast<const void*>(k), cudaFuncAttributeMaxDynamicSharedMemorySize, p.smem);
   if (e != cudaSuccess) return cuda_status(e);
   count_launch();
-  return cuda_status(launch_pdl(k, dim3(p.ctas), dim3(kThreads), p.smem, stream, map256, map64, map16, g));
+  return cuda_status(launch_pdl(k, dim3(p.ctas), dim3(kThreads), p.smem, stream, maps, g));
 }
 
 }  // namespace

@@ -553,6 +553,19 @@ bool make_map_f16_sw128(CUtensorMap* map, const void* base, int64_t cols, int64_
   return r == CUDA_SUCCESS;
 }
 
+bool make_map_f16_steps(CUtensorMap* map, const void* base, int64_t steps, int64_t rows, int64_t ld, int box_rows,
+                        int box_steps) {
+  auto fn = encode_fn();
+  if (!fn) return false;
+  cuuint64_t dims[3] = {64, static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(steps)};
+  cuuint64_t strides[2] = {static_cast<cuuint64_t>(ld * 2), 128};
+  cuuint32_t box[3] = {64, static_cast<cuuint32_t>(box_rows), static_cast<cuuint32_t>(box_steps)};
+  cuuint32_t estr[3] = {1, 1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 bool make_map_u8_sw128(CUtensorMap* map, const void* base, int64_t cols, int64_t rows, int64_t ld, int box_rows) {
   auto fn = encode_fn();
   if (!fn) return false;

@@ -162,6 +162,10 @@ vq_status launch_gemv(const Layer& L, const GemvPlan& plan, const void* x, bool 
 bool make_map_f16_sw128(CUtensorMap* map, const void* base, int64_t cols, int64_t rows, int64_t ld,
                         int box_rows);
 
+// The same tensor [rows][64 * steps] as steps of 64 columns: box {64, box_rows,
+// box_steps}, so that one load brings the tiles of several steps.
+bool make_map_f16_steps(CUtensorMap* map, const void* base, int64_t steps, int64_t rows, int64_t ld, int box_rows,
+                        int box_steps);
 // The same for bytes: box {128, box_rows} (box_rows <= 256).
 bool make_map_u8_sw128(CUtensorMap* map, const void* base, int64_t cols, int64_t rows, int64_t ld, int box_rows);
 
