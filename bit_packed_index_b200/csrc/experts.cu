@@ -2,6 +2,7 @@
 // ragged groups of rows that a router made (include/vq_experts.h).
 #include <algorithm>
 #include <cstdlib>
+#include <type_traits>
 
 #include "codebook.cuh"
 #include "sm100.cuh"
@@ -187,7 +188,8 @@ struct Args {
   int staged;               // bit m: book m in shared memory
   int copies;               // bit m: eight copies of it
   int off_book[2];          // its first byte behind the rings
-  int off_table;            // the same of the borders' table
+  int off_table;            // the same of the borders' tables
+  int off_scales;           // the same of the rows' scales
   const float* xe;
   const float* xsum;
   void* y;
@@ -236,51 +238,60 @@ __device__ __forceinline__ bool barrier_all(int id, int count, bool ok) {
   return r != 0;
 }
 
-// The line of work.  off: group borders (clamped), first: token tiles before
-// each expert, both in shared memory.
-struct Line {
-  const int* off;
-  const int* first;
-  int experts, row_tiles, nkt, tokens;
-  int acc;                  // rows of an accumulator: a tile of more takes two
-  int ctas;                 // CTAs with a share
-  int64_t steps;            // of all tiles
-
-  __device__ __forceinline__ int64_t border(int c) const {      // first step of CTA c's share
-    if (c <= 0) return 0;
-    if (c >= ctas) return steps;
-    const int64_t b = steps * c / ctas;
-    const int64_t tile = b / nkt;
-    const int in = static_cast<int>(b - tile * nkt);
-    if (in < kSnap) return tile * nkt;
-    if (nkt - in < kSnap) return (tile + 1) * nkt;
-    return b;
+// A place on the line of work: step kt of a tile (kt < steps of a tile).
+struct Place {
+  int tile, kt;
+  __device__ __forceinline__ bool operator==(const Place& o) const { return tile == o.tile && kt == o.kt; }
+  __device__ __forceinline__ bool operator<(const Place& o) const {
+    return tile < o.tile || (tile == o.tile && kt < o.kt);
   }
 };
 
-// One CTA's part of one tile.
+// The line of work, its tables in shared memory: off, the group borders
+// (clamped); first, the token tiles before each expert; border[c], where CTA
+// c's share starts (border[CTAs]: the end).
+struct Line {
+  const int* off;
+  const int* first;
+  const Place* border;
+  int experts, row_tiles, nkt;
+  int acc;                  // rows of an accumulator: a tile of more takes two
+};
+
+// First place of CTA c's share when `ctas` of them divide `tiles` tiles.
+__device__ __forceinline__ Place share_border(int64_t tiles, int nkt, int ctas, int c) {
+  if (c >= ctas) return {static_cast<int>(tiles), 0};
+  const int64_t b = tiles * nkt * c / ctas;
+  int tile = static_cast<int>(b / nkt), kt = static_cast<int>(b - static_cast<int64_t>(tile) * nkt);
+  if (kt < kSnap) kt = 0;
+  else if (nkt - kt < kSnap) ++tile, kt = 0;
+  return {tile, kt};
+}
+
+// One CTA's part of one tile: from `at` to the tile's end or `end`, where it
+// moves `at`.
 struct Part {
-  int64_t tile;
-  int expert, row0, r0, live, n;     // first W row; first grouped row, its rows, those padded to 16
+  int tile, expert, row0, r0, live, n;     // first W row; first grouped row, its rows, those padded to 16
   int kt0, kt1;
   int acc;
 
-  __device__ __forceinline__ Part(const Line& l, int64_t at, int64_t end) {
+  __device__ __forceinline__ Part(const Line& l, Place& at, const Place& end) {
     acc = l.acc;
-    tile = at / l.nkt;
-    kt0 = static_cast<int>(at - tile * l.nkt);
-    kt1 = static_cast<int>(min(static_cast<int64_t>(l.nkt), kt0 + (end - at)));
+    tile = at.tile;
+    kt0 = at.kt;
+    kt1 = at.tile == end.tile ? end.kt : l.nkt;
+    at = at.tile == end.tile ? end : Place{at.tile + 1, 0};
     // the expert: the last one whose tiles start at or before this one
     int lo = 0, hi = l.experts - 1;
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
-      if (static_cast<int64_t>(l.first[mid]) * l.row_tiles <= tile) lo = mid;
+      if (l.first[mid] * l.row_tiles <= tile) lo = mid;
       else hi = mid - 1;
     }
     expert = lo;
     const int tt = l.first[lo + 1] - l.first[lo];
-    const int64_t in = tile - static_cast<int64_t>(l.first[lo]) * l.row_tiles;   // row tile major
-    const int rt = static_cast<int>(in / tt), j = static_cast<int>(in - static_cast<int64_t>(rt) * tt);
+    const int in = tile - l.first[lo] * l.row_tiles;           // row tile major
+    const int rt = in / tt, j = in - rt * tt;
     const int count = l.off[lo + 1] - l.off[lo];
     const int per = ((count + tt - 1) / tt + 15) / 16 * 16;
     row0 = rt * kRowTile;
@@ -396,6 +407,32 @@ struct Maps {
   CUtensorMap m[kBoxes];
 };
 
+// y of one output (its column in y: yo) for `n` of sixteen rows from their
+// sums: s v 2^e + t sum x + b.  scales: 2^e and sum x of the rows, in shared
+// memory.  The type is a template argument: a branch on it per value, with the
+// single warp that each scheduler has for this, made the store of a tile take
+// longer than its products.
+template <int YT>
+__device__ __forceinline__ void store_rows(uint8_t* yo, int64_t ldb, const float (&v)[16], int n, const float4* scales,
+                                           float sc, float tb, float ob) {
+  using T = typename std::conditional<YT == VQ_FP32, float, uint16_t>::type;
+#pragma unroll
+  for (int i = 0; i < 16; i += 2) {
+    const float4 e = scales[i / 2];
+    const float a = sc * (v[i] * e.x) + (tb * e.y + ob), b = sc * (v[i + 1] * e.z) + (tb * e.w + ob);
+    T x, y;
+    if constexpr (YT == VQ_FP32) {
+      x = a;
+      y = b;
+    } else {
+      x = YT == VQ_FP16 ? f2h(a) : f2bf(a);
+      y = YT == VQ_FP16 ? f2h(b) : f2bf(b);
+    }
+    if (i < n) *reinterpret_cast<T*>(yo + i * ldb) = x;
+    if (i + 1 < n) *reinterpret_cast<T*>(yo + (i + 1) * ldb) = y;
+  }
+}
+
 // Where a book is read from.  A staged entry takes 16 bytes a chunk (eight
 // values); a small book is kept eight times over, entry i's copies side by
 // side, so that the eight lanes of a shared-memory phase read eight different
@@ -406,16 +443,26 @@ struct Book {
   const uint16_t* global;   // not staged: rows of d halves
 };
 
-// Chunk q of entry i of a book that may be staged or not, d of any size.
-__device__ __forceinline__ uint4 any_centroid(const Book& b, bool staged, int d, uint32_t i, int q) {
-  if (staged) return lds128(b.smem + (i << b.shift) + 16 * q);
-  const uint16_t* r = b.global + static_cast<size_t>(i) * d + 8 * q;
+// Chunk q (values 8 q .. 8 q + 7, zeros past d) of entry i of a book of rows of d halves.
+__device__ __forceinline__ uint4 global_chunk(const uint16_t* book, int d, uint32_t i, int q) {
+  const uint16_t* r = book + static_cast<size_t>(i) * d + 8 * q;
   if (d % 8 == 0) return __ldg(reinterpret_cast<const uint4*>(r));
   uint32_t w[4] = {0u, 0u, 0u, 0u};
+  if (d % 2 == 0) {
 #pragma unroll
-  for (int e = 0; e < 8; ++e)
-    if (8 * q + e < d) w[e >> 1] |= static_cast<uint32_t>(__ldg(r + e)) << (16 * (e & 1));
+    for (int e = 0; e < 4; ++e)
+      if (8 * q + 2 * e < d) w[e] = __ldg(reinterpret_cast<const uint32_t*>(r) + e);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (8 * q + e < d) w[e >> 1] |= static_cast<uint32_t>(__ldg(r + e)) << (16 * (e & 1));
+  }
   return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// The same of a book that may be staged.
+__device__ __forceinline__ uint4 any_centroid(const Book& b, bool staged, int d, uint32_t i, int q) {
+  return staged ? lds128(b.smem + (i << b.shift) + 16 * q) : global_chunk(b.global, d, i, q);
 }
 
 // W tiles whose rows pass through registers anyway (books in shared memory) lie
@@ -448,6 +495,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   volatile int* abort_flag = &ctrl->abort;
   int* s_off = reinterpret_cast<int*>(books + g.off_table);    // [experts + 1] borders
   int* s_first = s_off + n_experts + 1;                        // [experts + 1] token tiles in front
+  Place* s_border = reinterpret_cast<Place*>(s_first + n_experts + 1);   // [CTAs + 1]
+  float2* s_scales = reinterpret_cast<float2*>(books + g.off_scales);    // [2][tokens]
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < g.na; ++s) mbar_init(&ctrl->fulla[s], kProducers / 32 / kGroups);
@@ -502,18 +551,24 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = uniform(ctrl->tmem);
+  {
+    const int64_t tiles = static_cast<int64_t>(s_first[n_experts]) * g.row_tiles;
+    const int ctas = static_cast<int>(
+        max(static_cast<int64_t>(1), min(static_cast<int64_t>(gridDim.x), tiles * g.nkt / kMinSteps)));
+    for (int c = threadIdx.x; c <= static_cast<int>(gridDim.x); c += kThreads)
+      s_border[c] = share_border(tiles, g.nkt, ctas, c);
+  }
+  __syncthreads();
   Line line;
   line.off = s_off;
   line.first = s_first;
+  line.border = s_border;
   line.experts = n_experts;
   line.row_tiles = g.row_tiles;
   line.nkt = g.nkt;
-  line.tokens = g.tokens;
   line.acc = kAcc;
-  line.steps = static_cast<int64_t>(s_first[n_experts]) * g.row_tiles * g.nkt;
-  line.ctas = static_cast<int>(max(static_cast<int64_t>(1), min(static_cast<int64_t>(gridDim.x), line.steps / kMinSteps)));
   const int cta = blockIdx.x;
-  const int64_t from = line.border(cta), to = line.border(cta + 1);
+  const Place from = s_border[cta], to = s_border[cta + 1];
   const int nbuf = g.tokens <= kAcc ? 2 : 1;         // accumulators in turn
   const uint32_t tmem_a = tmem + 2 * kAcc;           // W steps of 32 columns
 
@@ -523,9 +578,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     asm volatile("griddepcontrol.wait;" ::: "memory");
     int q = 0, qp = 0, issued = 0;                    // x slot, its phase, loads issued
     bool stop = false;
-    for (int64_t at = from; at < to && !stop;) {
+    for (Place at = from; at < to && !stop;) {
       const Part t(line, at, to);
-      at += t.kt1 - t.kt0;
       const int n0 = uniform(t.half_rows(0)), n1 = uniform(t.n) - n0, r0 = uniform(t.r0);
       const int kt1 = uniform(t.kt1), b0 = box_of(n0);
       for (int kt = uniform(t.kt0); kt < kt1 && !stop; kt += g.xk) {
@@ -567,9 +621,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     int q = 0, qp = 0, s = 0, sp = 0, it = 0, step = 0;
     bool stop = false;
-    for (int64_t at = from; at < to && !stop; ++it) {
+    for (Place at = from; at < to && !stop; ++it) {
       const Part t(line, at, to);
-      at += t.kt1 - t.kt0;
+      // two accumulators in turn, or the halves of one tile after another: `acce`
+      // of a half tells that the epilogue has read it
       const int buf = it % nbuf;
       if (it >= nbuf && !warp_wait(&ctrl->acce[buf], ((it / nbuf) & 1) ^ 1, abort_flag, g.status, g.budget)) break;
       tc_fence_after();
@@ -640,7 +695,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             sp ^= 1;
           }
           for (int h = 0; h < halves; ++h) {
-            if (!readyx && !warp_wait(&ctrl->fullx[q], qp, abort_flag, g.status, g.budget)) {
+            if ((!readyx && !warp_wait(&ctrl->fullx[q], qp, abort_flag, g.status, g.budget)) ||
+                (h == 1 && add == 0 && it > 0 &&
+                 !warp_wait(&ctrl->acce[1], (it & 1) ^ 1, abort_flag, g.status, g.budget))) {
               stop = true;
               break;
             }
@@ -677,11 +734,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp >= 4 && warp < 8) {                 // epilogue: lane quarter warp & 3, one W row per thread
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int lq = warp & 3, r = 32 * lq + lane;
+    const int64_t slot_size = static_cast<int64_t>(g.tokens) * kRowTile;
+    const int64_t ldb = g.ldy * (g.yt == VQ_FP32 ? 4 : 2);
     int it = 0;
-    for (int64_t at = from; at < to; ++it) {
+    for (Place at = from; at < to; ++it) {
       const Part t(line, at, to);
       const bool whole = t.kt0 == 0 && t.kt1 == g.nkt;
-      at += t.kt1 - t.kt0;
       const int buf = it % nbuf;
       const int o = t.row0 + r;
       const Layer L = expert_layer(g.E, t.expert);
@@ -689,94 +747,82 @@ __global__ void __launch_bounds__(kThreads, 1)
       const float sc = live && L.scale ? h2f(__ldg(L.scale + o)) : 1.0f;
       const float tb = live && L.bias ? h2f(__ldg(L.bias + o)) : 0.0f;
       const float ob = live ? out_bias_of(L.ob, o) : 0.0f;
+      // the rows' scales and sums, in the table that the tile before last used
+      float2* scales = s_scales + (it & 1) * g.tokens;
+      for (int i = r; i < t.n; i += 128)
+        scales[i] = i < t.live ? make_float2(g.xe[t.r0 + i], g.xsum[t.r0 + i]) : make_float2(0.0f, 0.0f);
+      uint8_t* yo = static_cast<uint8_t*>(g.y) + t.r0 * ldb + static_cast<int64_t>(o) * (g.yt == VQ_FP32 ? 4 : 2);
+      auto store16 = [&](const float (&v)[16], int c) {
+        const int n = live ? t.live - c : 0;
+        const float4* e = reinterpret_cast<const float4*>(scales + c);
+        uint8_t* p = yo + c * ldb;
+        if (g.yt == VQ_BF16) store_rows<VQ_BF16>(p, ldb, v, n, e, sc, tb, ob);
+        else if (g.yt == VQ_FP16) store_rows<VQ_FP16>(p, ldb, v, n, e, sc, tb, ob);
+        else store_rows<VQ_FP32>(p, ldb, v, n, e, sc, tb, ob);
+      };
       // the four warps go on together or not at all (they meet at barriers below)
       if (!barrier_all(1, 128, warp_wait(&ctrl->accf[buf], (it / nbuf) & 1, abort_flag, g.status, g.budget))) break;
       tc_fence_after();
       const uint32_t acc0 = tmem + buf * kAcc + (static_cast<uint32_t>(32 * lq) << 16);
       const int n0 = t.half_rows(0);
-      // rows c .. c + 15 of the tile start at tensor-memory column c, or kAcc + c - n0 in the second half
-      auto column = [&](int c) { return acc0 + (c < n0 ? c : kAcc + c - n0); };
-      if (whole) {
-        for (int c = 0; c < t.live; c += 16) {
-          uint32_t acc[16];
-          tmem_ld16(column(c), acc);
-          float xel = 0.0f, xsl = 0.0f;
-          if (c + (lane & 15) < t.live) {
-            xel = g.xe[t.r0 + c + (lane & 15)];
-            xsl = g.xsum[t.r0 + c + (lane & 15)];
-          }
-          tmem_wait_ld();
-          const int n = min(16, t.live - c);
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const float e = __shfl_sync(0xffffffffu, xel, i), x = __shfl_sync(0xffffffffu, xsl, i);
-            if (live && i < n)
-              store_out(g.y, g.yt, static_cast<int64_t>(t.r0 + c + i) * g.ldy + o,
-                        sc * (__uint_as_float(acc[i]) * e) + tb * x + ob);
+      // a shared tile: the sums to this CTA's slot (1: it starts the tile, 0: it goes on with it)
+      float* mine = g.part + (2 * static_cast<int64_t>(cta) + (t.kt0 == 0 ? 1 : 0)) * slot_size + r;
+      for (int c = 0; c < t.n; c += 16) {
+        uint32_t acc[16];
+        // rows c .. c + 15 start at tensor-memory column c, or kAcc + c - n0 in the second half
+        tmem_ld16(acc0 + (c < n0 ? c : kAcc + c - n0), acc);
+        tmem_wait_ld();
+        if (c + 16 == t.n || (nbuf == 1 && c + 16 == n0)) {      // a half is read
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) {
+            if (nbuf == 2) mbar_arrive(&ctrl->acce[buf]);
+            if (nbuf == 1 && c + 16 == n0) mbar_arrive(&ctrl->acce[0]);
+            if (nbuf == 1 && c + 16 == t.n) mbar_arrive(&ctrl->acce[1]);
           }
         }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&ctrl->acce[buf]);
-        continue;
-      }
-      // a shared tile: the sums to this CTA's slot (1: it starts the tile, 0: it goes on with it)
-      const int64_t slot_size = static_cast<int64_t>(g.tokens) * kRowTile;
-      float* mine = g.part + (2 * static_cast<int64_t>(cta) + (t.kt0 == 0 ? 1 : 0)) * slot_size;
-      for (int c = 0; c < t.live; c += 16) {
-        uint32_t acc[16];
-        tmem_ld16(column(c), acc);
-        tmem_wait_ld();
-        const int n = min(16, t.live - c);
+        float v[16];
 #pragma unroll
-        for (int i = 0; i < 16; ++i)
-          if (i < n) __stcg(mine + (c + i) * kRowTile + r, __uint_as_float(acc[i]));
+        for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(acc[i]);
+        if (whole) {
+          store16(v, c);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) __stcg(mine + (c + i) * kRowTile, v[i]);
+        }
       }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&ctrl->acce[buf]);
+      if (whole) continue;
       // the CTAs of the tile: from the one whose share holds its first step to
       // the one with its last
       int c0 = cta, c1 = cta;
-      const int64_t begin = t.tile * g.nkt, end = begin + g.nkt;
-      while (c0 > 0 && line.border(c0) > begin) --c0;
-      while (line.border(c1 + 1) < end) ++c1;
+      const Place begin = {t.tile, 0}, end = {t.tile + 1, 0};
+      while (c0 > 0 && begin < s_border[c0]) --c0;
+      while (s_border[c1 + 1] < end) ++c1;
       __threadfence();
       asm volatile("bar.sync 1, 128;" ::: "memory");
       if (r == 0) {
         int parts = 0;                                // shares that are not empty
-        for (int c = c0; c <= c1; ++c) parts += line.border(c + 1) > line.border(c) ? 1 : 0;
+        for (int c = c0; c <= c1; ++c) parts += s_border[c + 1] == s_border[c] ? 0 : 1;
         ctrl->last = atomicAdd(g.joined + c0, 1) == parts - 1;
         __threadfence();
       }
       asm volatile("bar.sync 1, 128;" ::: "memory");
       if (ctrl->last) {
         // sixteen rows at a time, so that their loads are in flight together
-        for (int c = 0; c < t.live; c += 16) {
-          const int n = min(16, t.live - c);
+        for (int c = 0; c < t.n; c += 16) {
           float v[16];
 #pragma unroll
           for (int i = 0; i < 16; ++i) v[i] = 0.0f;
           for (int k = c0; k <= c1; ++k) {
-            if (line.border(k + 1) == line.border(k)) continue;
+            if (s_border[k + 1] == s_border[k]) continue;
             const float* part = g.part + (2 * static_cast<int64_t>(k) + (k == c0 ? 1 : 0)) * slot_size + c * kRowTile + r;
             float u[16];
 #pragma unroll
-            for (int i = 0; i < 16; ++i) u[i] = i < n ? __ldcg(part + i * kRowTile) : 0.0f;
+            for (int i = 0; i < 16; ++i) u[i] = __ldcg(part + i * kRowTile);
 #pragma unroll
             for (int i = 0; i < 16; ++i) v[i] += u[i];
           }
-          float xel = 0.0f, xsl = 0.0f;
-          if ((lane & 15) < n) {
-            xel = g.xe[t.r0 + c + (lane & 15)];
-            xsl = g.xsum[t.r0 + c + (lane & 15)];
-          }
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const float e = __shfl_sync(0xffffffffu, xel, i), x = __shfl_sync(0xffffffffu, xsl, i);
-            if (live && i < n)
-              store_out(g.y, g.yt, static_cast<int64_t>(t.r0 + c + i) * g.ldy + o, sc * (v[i] * e) + tb * x + ob);
-          }
+          store16(v, c);
         }
       }
       asm volatile("bar.sync 1, 128;" ::: "memory");  // `last` is read before the next tile sets it
@@ -796,9 +842,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     int staged_expert = -1;
     int gs = 0;                                       // steps of this CTA's earlier tiles
     bool stop = false;                                // a warp that gave up still meets the others where books change
-    for (int64_t at = from; at < to;) {
+    for (Place at = from; at < to;) {
       const Part t(line, at, to);
-      at += t.kt1 - t.kt0;
       const Layer L = expert_layer(g.E, t.expert);
       book[0].global = L.book[0];
       book[1].global = L.book[1];
@@ -827,21 +872,25 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint16_t* src = L.book[m];
           const bool copies = (g.copies >> m) & 1;
           const uint32_t dst = smem_addr(books) + g.off_book[m];
-          const int total = (ch << L.b[m]) << (copies ? 3 : 0);   // 16-byte chunks to write
-          for (int i = pt; i < total; i += kProducers) {
-            const int q = i & (ch - 1), e = copies ? i / (8 * ch) : i / ch;
-            uint4 v;
-            if (L.d % 8 == 0) {
-              v = __ldg(reinterpret_cast<const uint4*>(src + static_cast<int64_t>(e) * L.d + 8 * q));
-            } else {
-              uint32_t w[4] = {0u, 0u, 0u, 0u};
+          const int chunks = ch << L.b[m];            // 16-byte chunks of the book
+          for (int i0 = pt; i0 < chunks; i0 += 4 * kProducers) {
+            uint4 v[4];                               // loads in flight together
 #pragma unroll
-              for (int x = 0; x < 8; ++x)
-                if (8 * q + x < L.d)
-                  w[x >> 1] |= static_cast<uint32_t>(__ldg(src + static_cast<int64_t>(e) * L.d + 8 * q + x)) << (16 * (x & 1));
-              v = make_uint4(w[0], w[1], w[2], w[3]);
+            for (int u = 0; u < 4; ++u) {
+              const int i = i0 + u * kProducers;
+              if (i < chunks) v[u] = global_chunk(src, L.d, i / ch, i & (ch - 1));
             }
-            sts128(dst + i * 16, v);
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+              const int i = i0 + u * kProducers;
+              if (i >= chunks) break;
+              if (copies) {
+#pragma unroll
+                for (int c = 0; c < 8; ++c) sts128(dst + ((i / ch * 8 + c) * ch + (i & (ch - 1))) * 16, v[u]);
+              } else {
+                sts128(dst + i * 16, v[u]);
+              }
+            }
           }
         }
         asm volatile("bar.sync 2, 512;" ::: "memory");
@@ -1004,7 +1053,7 @@ size_t round256(size_t b) { return (b + 255) / 256 * 256; }
 struct Plan {
   int nkt, row_tiles, tokens, ctas;
   int64_t kp;
-  int na, nx, xk, xslot, staged, copies, off_book[2], off_table, smem;
+  int na, nx, xk, xslot, staged, copies, off_book[2], off_table, off_scales, smem;
   size_t off_xe, off_sum, off_joined, off_xh, off_part, total;
 };
 
@@ -1037,7 +1086,9 @@ bool fit(const Experts& E, int m, int staged, int copies, int tokens, Plan* p) {
     if (staged & (1 << b)) off += ((1 << L.b[b]) * 16 * ch) << ((copies >> b) & 1 ? 3 : 0);
   }
   p->off_table = off;
-  off += 8 * (E.e + 1);
+  off += 8 * (E.e + 1) + 8 * (device_sm_count() + 1);
+  p->off_scales = off = (off + 15) / 16 * 16;
+  off += 2 * 8 * std::min((m + 15) / 16 * 16, tokens);
   const int room = device_smem_optin() - 2048 - off;
   const bool in_tmem = w_in_tmem(widths_of(L, staged).b1);
   const int acc = acc_rows(in_tmem), atile = in_tmem ? 0 : kATile;
@@ -1100,6 +1151,13 @@ Plan plan_experts(const Experts& E, int m) {
   return p;
 }
 
+// Tiles are counted in 31 bits: at most (experts + m / 16) of grouped rows
+// (tiles hold 32 rows or all m) times the row tiles of W.
+bool too_many_tiles(const Experts& E, int m) {
+  const int64_t row_tiles = (static_cast<int64_t>(E.L.n) + kRowTile - 1) / kRowTile;
+  return (E.e + static_cast<int64_t>(m) / 16) * row_tiles > 0x7FFFFFFFLL;
+}
+
 size_t experts_bytes(const Experts& E, int m) { return E.L.kin == 0 ? 256 : plan_experts(E, m).total; }
 
 long long wait_budget() {
@@ -1148,6 +1206,7 @@ vq_status launch_gemm_experts(const Experts& E, const void* x, bool x_fp16, int 
   g.off_book[0] = p.off_book[0];
   g.off_book[1] = p.off_book[1];
   g.off_table = p.off_table;
+  g.off_scales = p.off_scales;
   float* xe = reinterpret_cast<float*>(w + p.off_xe);
   float* xsum = reinterpret_cast<float*>(w + p.off_sum);
   g.xe = xe;
@@ -1189,7 +1248,7 @@ vq_status vq_gemm_experts_workspace_size(const vq_experts_desc* experts, int32_t
   vq_status st = check_experts(experts, &E);
   if (st != VQ_OK) return st;
   if (m < 0) return VQ_ERR_INVALID_ARG;
-  if (m > kMaxGroupedRows) return VQ_ERR_UNSUPPORTED;
+  if (m > kMaxGroupedRows || too_many_tiles(E, m)) return VQ_ERR_UNSUPPORTED;
   *bytes = m == 0 || E.L.n == 0 ? 0 : experts_bytes(E, m);
   return VQ_OK;
 }
@@ -1203,7 +1262,7 @@ vq_status vq_gemm_experts(const vq_experts_desc* experts, const void* x, vq_dtyp
   if (m < 0 || x_rows < 0 || !(x_dtype == VQ_BF16 || x_dtype == VQ_FP16) ||
       !(y_dtype == VQ_BF16 || y_dtype == VQ_FP16 || y_dtype == VQ_FP32) || ldx < E.L.kin || ldy < E.L.n)
     return VQ_ERR_INVALID_ARG;
-  if (m > kMaxGroupedRows) return VQ_ERR_UNSUPPORTED;
+  if (m > kMaxGroupedRows || too_many_tiles(E, m)) return VQ_ERR_UNSUPPORTED;
   if (!rows && x_rows < m) return VQ_ERR_INVALID_ARG;
   if (m == 0 || E.L.n == 0) return VQ_OK;
   if (!y || !offsets || (!x && x_rows > 0 && E.L.kin > 0)) return VQ_ERR_INVALID_ARG;

@@ -88,11 +88,30 @@ __device__ __forceinline__ bool bounded_wait(uint64_t* bar, uint32_t parity, vol
   }
 }
 
-// bounded_wait by a whole warp, with one answer for all lanes.  (All lanes
-// poll: one lane polling while the others wait for it measured slower.)
+// bounded_wait by a whole warp, with one answer for all lanes.  The warp is
+// suspended for up to 20 us at a time: warps that poll without it take the
+// issue slots and the shared-memory queue of those that have work.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort, int* status,
                                           long long budget) {
-  return __all_sync(0xffffffffu, bounded_wait(bar, parity, abort, status, budget));
+  if (__all_sync(0xffffffffu, mbar_test_wait(bar, parity))) return true;
+  const long long t0 = clock64();
+  for (;;) {
+    uint32_t ok = 0;
+    if (budget > 0)
+      asm volatile(
+          "{\n\t.reg .pred p;\n\t"
+          "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+          "selp.u32 %0, 1, 0, p;\n\t}\n"
+          : "=r"(ok)
+          : "r"(smem_addr(bar)), "r"(parity), "r"(20000)
+          : "memory");
+    if (__all_sync(0xffffffffu, ok != 0)) return true;
+    if (__any_sync(0xffffffffu, budget <= 0 || *abort || clock64() - t0 > budget)) {
+      *abort = 1;
+      if (status) atomicExch(status, static_cast<int>(VQ_ERR_TIMEOUT));
+      return false;
+    }
+  }
 }
 
 // Issuing loops run on a whole warp, the asynchronous instructions under

@@ -92,7 +92,8 @@ VQ_API vq_status vq_gemm_experts_workspace_size(const vq_experts_desc* experts, 
  * on the sizes and the group sizes only, so repeated calls agree bit for bit.
  * A row of x that holds an infinity or a NaN has non-finite products; the
  * other rows are not touched by it.
- * Errors: VQ_ERR_INVALID_ARG, VQ_ERR_UNSUPPORTED (m > 2^24), VQ_ERR_ALIGNMENT
+ * Errors: VQ_ERR_INVALID_ARG, VQ_ERR_UNSUPPORTED (m > 2^24, or (n_experts +
+ * m / 16) * ceil(N / 128) >= 2^31), VQ_ERR_ALIGNMENT
  * (arrays; x and y to their element sizes), VQ_ERR_WORKSPACE, VQ_ERR_CUDA.
  */
 VQ_API vq_status vq_gemm_experts(const vq_experts_desc* experts, const void* x, vq_dtype x_dtype,
