@@ -224,20 +224,6 @@ __device__ __forceinline__ uint4 hadd8(const uint4& a, const uint4& b) {
   return make_uint4(hadd2_u32(a.x, b.x), hadd2_u32(a.y, b.y), hadd2_u32(a.z, b.z), hadd2_u32(a.w, b.w));
 }
 
-// True on all threads of named barrier `id` (count threads) if `ok` is on all.
-__device__ __forceinline__ bool barrier_all(int id, int count, bool ok) {
-  uint32_t r;
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\t"
-      "setp.ne.b32 q, %3, 0;\n\t"
-      "bar.red.and.pred p, %1, %2, q;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}\n"
-      : "=r"(r)
-      : "r"(id), "r"(count), "r"(static_cast<uint32_t>(ok))
-      : "memory");
-  return r != 0;
-}
-
 // A place on the line of work: step kt of a tile (kt < steps of a tile).
 struct Place {
   int tile, kt;

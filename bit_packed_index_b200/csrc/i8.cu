@@ -10,6 +10,7 @@
 // element in 5000 takes that path; the kernel stays at the memory's speed.
 #include <algorithm>
 #include <cstdlib>
+#include <type_traits>
 
 #include "sm100.cuh"
 #include "vq_i8.h"
@@ -200,6 +201,7 @@ constexpr int kRows = 128;                 // output channels per CTA
 constexpr int kStepBytes = 128;            // values of k per step
 constexpr int kWTile = kRows * kStepBytes;
 constexpr int kMaxStages = 8;
+constexpr int kCtrlBytes = 3072;           // control block in front of the stages (a multiple of 1024)
 constexpr long long kDrain = 1LL << 26;    // SM clocks: far above any load's latency
 
 __device__ __forceinline__ uint8_t* align1024(uint8_t* p) {
@@ -212,6 +214,34 @@ __device__ __forceinline__ float i8_out(int acc, float w, float s, float b) {
   return __fadd_rn(__fmul_rn(__fmul_rn(__int2float_rn(acc), w), s), b);
 }
 
+// Outputs of one channel (its column in y: yo) for `n` of sixteen rows.  The
+// output type is a template argument: the epilogue is one warp per scheduler,
+// which a branch per value would keep longer than the products take.
+template <int YT>
+__device__ __forceinline__ void store_rows(uint8_t* yo, int64_t ldb, const uint32_t* acc, int n, const float4* scales,
+                                           float w, float b) {
+  using T = typename std::conditional<YT == VQ_FP32, float, uint16_t>::type;
+#pragma unroll
+  for (int i = 0; i < 16; i += 4) {
+    const float4 e = scales[i / 4];
+    const float s[4] = {e.x, e.y, e.z, e.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float v = i8_out(static_cast<int>(acc[i + j]), w, s[j], b);
+      T x;
+      if constexpr (YT == VQ_FP32) x = v;
+      else x = YT == VQ_FP16 ? f2h(v) : f2bf(v);
+      if (i + j < n) *reinterpret_cast<T*>(yo + (i + j) * ldb) = x;
+    }
+  }
+}
+__device__ __forceinline__ void store_rows(vq_dtype yt, uint8_t* yo, int64_t ldb, const uint32_t* acc, int n,
+                                           const float4* scales, float w, float b) {
+  if (yt == VQ_BF16) store_rows<VQ_BF16>(yo, ldb, acc, n, scales, w, b);
+  else if (yt == VQ_FP16) store_rows<VQ_FP16>(yo, ldb, acc, n, scales, w, b);
+  else store_rows<VQ_FP32>(yo, ldb, acc, n, scales, w, b);
+}
+
 // ---- one to 64 rows: W's bytes are the bound ------------------------------------
 // A cluster of S CTAs shares a tile of 128 outputs, each CTA a run of k, so
 // that even a layer of 1024 outputs keeps most SMs loading.  The partial sums
@@ -221,7 +251,9 @@ struct NarrowCtrl {
   uint64_t full[kMaxStages], empty[kMaxStages], acc;
   uint32_t tmem;
   int abort;
+  alignas(16) float scales[64];            // activation scales
 };
+static_assert(sizeof(NarrowCtrl) <= kCtrlBytes, "control block");
 constexpr int kNarrowRows = 64;
 constexpr int kNarrowThreads = 192;        // warp 0: loads, warp 1: products, warps 2-5: epilogue
 
@@ -231,7 +263,7 @@ __global__ void __launch_bounds__(kNarrowThreads) gemm_i8_narrow_kernel(const __
   extern __shared__ uint8_t smem_raw[];
   uint8_t* base = align1024(smem_raw);
   NarrowCtrl* ctrl = reinterpret_cast<NarrowCtrl*>(base);
-  uint8_t* stages = base + 1024;
+  uint8_t* stages = base + kCtrlBytes;
   const int stage = kWTile + g.tn * kStepBytes;
   const int warp = uniform(static_cast<int>(threadIdx.x >> 5)), lane = threadIdx.x & 31;
   const int splits = gridDim.y, split = blockIdx.y;          // the cluster spans the grid's y
@@ -317,20 +349,21 @@ __global__ void __launch_bounds__(kNarrowThreads) gemm_i8_narrow_kernel(const __
     }
   } else {
     const int lq = warp & 3, r = 32 * lq + lane, o = row0 + r;
+    if (r < kNarrowRows) ctrl->scales[r] = r < g.m ? g.qs[r] : 0.0f;
     const bool ok = warp_wait(&ctrl->acc, 0, abort_flag, g.status, g.budget);
+    asm volatile("bar.sync 1, 128;" ::: "memory");           // the scales of all rows are there
     tc_fence_after();
     const uint32_t t = tmem + (static_cast<uint32_t>(32 * lq) << 16);
     if (splits == 1) {
       const bool live = ok && o < g.n;
       const float w = live ? g.ws[o] : 0.0f, b = live ? out_bias_of(g.ob, o) : 0.0f;
+      const int64_t ldb = g.ldy * (g.yt == VQ_FP32 ? 4 : 2);
+      uint8_t* yo = static_cast<uint8_t*>(g.y) + static_cast<int64_t>(o) * (g.yt == VQ_FP32 ? 4 : 2);
       for (int c = 0; c < g.m; c += 16) {
         uint32_t acc[16];
         tmem_ld16(t + c, acc);
         tmem_wait_ld();
-#pragma unroll
-        for (int i = 0; i < 16; ++i)
-          if (live && c + i < g.m)
-            store_out(g.y, g.yt, (c + i) * g.ldy + o, i8_out(nkt ? static_cast<int>(acc[i]) : 0, w, __ldg(g.qs + c + i), b));
+        if (live) store_rows(g.yt, yo + c * ldb, ldb, acc, g.m - c, reinterpret_cast<const float4*>(ctrl->scales + c), w, b);
       }
     } else if (ok) {
       // partial sums to the (spent) stage memory, [row of x][128]
@@ -387,7 +420,9 @@ struct WideCtrl {
   uint64_t accf[2], acce[2];
   uint32_t tmem;
   int abort;
+  alignas(16) float scales[2][256];        // activation scales of a tile's rows, two tiles in turn
 };
+static_assert(sizeof(WideCtrl) <= kCtrlBytes, "control block");
 constexpr int kWideThreads = 256;          // warp 0: loads, warp 1: products, warps 4-7: epilogue
 constexpr int kWideTn = 256;
 constexpr uint32_t kWideCols = 512;
@@ -397,7 +432,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* base = align1024(smem_raw);
   WideCtrl* ctrl = reinterpret_cast<WideCtrl*>(base);
-  uint8_t* stages = base + 1024;
+  uint8_t* stages = base + kCtrlBytes;
   const int half = g.tn / 2;                                 // rows of q per CTA
   const int stage = kWTile + half * kStepBytes;
   const int warp = uniform(static_cast<int>(threadIdx.x >> 5)), lane = threadIdx.x & 31;
@@ -504,29 +539,34 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1)
       }
     }
   } else if (warp >= 4) {
-    const int lq = warp & 3;
+    const int lq = warp & 3, r = 32 * lq + lane;
+    const int64_t ldb = g.ldy * (g.yt == VQ_FP32 ? 4 : 2);
     int it = 0;
     for (int tile = pair; tile < tiles; tile += pairs, ++it) {
       const int buf = it & 1;
-      const int o = (tile / g.tiles_m) * 2 * kRows + rank * kRows + 32 * lq + lane;
+      const int o = (tile / g.tiles_m) * 2 * kRows + rank * kRows + r;
       const int t0 = (tile % g.tiles_m) * g.tn;
       const bool live = o < g.n;
       const float w = live ? __ldg(g.ws + o) : 0.0f, b = live ? out_bias_of(g.ob, o) : 0.0f;
-      if (!warp_wait(&ctrl->accf[buf], (it >> 1) & 1, abort_flag, g.status, g.budget)) break;
-      tc_fence_after();
+      for (int i = r; i < g.tn; i += 128) ctrl->scales[buf][i] = t0 + i < g.m ? g.qs[t0 + i] : 0.0f;
+      const bool ok = warp_wait(&ctrl->accf[buf], (it >> 1) & 1, abort_flag, g.status, g.budget);
+      // the table is written; no warp goes on alone (it would wait here for the others)
+      if (barrier_all(1, 128, ok)) {
+        tc_fence_after();
+      } else {
+        break;
+      }
       const int cols = min(g.tn, g.m - t0);
-      for (int c = 0; c < cols; c += 32) {
+      uint8_t* yo = static_cast<uint8_t*>(g.y) + t0 * ldb + static_cast<int64_t>(o) * (g.yt == VQ_FP32 ? 4 : 2);
+      for (int c = 0; c < g.tn; c += 32) {
+        if (c >= cols) break;
         uint32_t acc[32];
         tmem_ld32(tmem + buf * kWideTn + c + (static_cast<uint32_t>(32 * lq) << 16), acc);
-        const float sl = t0 + c + lane < g.m ? __ldg(g.qs + t0 + c + lane) : 0.0f;
         tmem_wait_ld();
-        const int n = min(32, cols - c);
-#pragma unroll
-        for (int i = 0; i < 32; ++i) {
-          const float s = __shfl_sync(0xffffffffu, sl, i);
-          if (live && i < n)
-            store_out(g.y, g.yt, static_cast<int64_t>(t0 + c + i) * g.ldy + o, i8_out(static_cast<int>(acc[i]), w, s, b));
-        }
+        if (!live) continue;
+        const float4* e = reinterpret_cast<const float4*>(ctrl->scales[buf] + c);
+        store_rows(g.yt, yo + c * ldb, ldb, acc, cols - c, e, w, b);
+        store_rows(g.yt, yo + (c + 16) * ldb, ldb, acc + 16, cols - c - 16, e + 4, w, b);
       }
       tc_fence_before();
       __syncwarp();
@@ -666,7 +706,7 @@ vq_status launch_gemm_i8(const I8Layer& L, const int8_t* q, int64_t ldq, const f
     const int tiles = (L.n + kRows - 1) / kRows;
     const int splits = narrow_splits(tiles, g.num_kt, sms);
     g.kt_per_split = (g.num_kt + splits - 1) / splits;
-    g.stages = std::min(kMaxStages, (device_smem_optin() / 2 - 2048 - 1024) / stage);   // two CTAs per SM
+    g.stages = std::min(kMaxStages, (device_smem_optin() / 2 - 1024 - kCtrlBytes - 1024) / stage);   // two CTAs per SM
     cfg.gridDim = dim3(tiles, splits);
     cfg.blockDim = dim3(kNarrowThreads);
     attr[1].id = cudaLaunchAttributeClusterDimension;
@@ -676,12 +716,12 @@ vq_status launch_gemm_i8(const I8Layer& L, const int8_t* q, int64_t ldq, const f
     cfg.numAttrs = 2;
     k = reinterpret_cast<const void*>(gemm_i8_narrow_kernel);
   } else {
-    g.stages = std::min(kMaxStages, (device_smem_optin() - 2048) / stage);
+    g.stages = std::min(kMaxStages, (device_smem_optin() - 1024 - kCtrlBytes) / stage);
     cfg.gridDim = dim3(2 * std::min(g.tiles_n * g.tiles_m, sms / 2));
     cfg.blockDim = dim3(kWideThreads);
     k = reinterpret_cast<const void*>(gemm_i8_wide_kernel);
   }
-  cfg.dynamicSmemBytes = 2048 + static_cast<size_t>(g.stages) * stage;
+  cfg.dynamicSmemBytes = 1024 + kCtrlBytes + static_cast<size_t>(g.stages) * stage;
   cudaError_t e = set_func_attr(k, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(cfg.dynamicSmemBytes));
   if (e != cudaSuccess) return cuda_status(e);
   count_launch();

@@ -133,6 +133,20 @@ __device__ __forceinline__ T uniform(T v) {
   return __shfl_sync(0xffffffffu, v, 0);
 }
 
+// True on all threads of named barrier `id` (count threads) if `ok` is on all.
+__device__ __forceinline__ bool barrier_all(int id, int count, bool ok) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.b32 q, %3, 0;\n\t"
+      "bar.red.and.pred p, %1, %2, q;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}\n"
+      : "=r"(r)
+      : "r"(id), "r"(count), "r"(static_cast<uint32_t>(ok))
+      : "memory");
+  return r != 0;
+}
+
 // Wait for the phase with the given parity whatever the abort flag says: used
 // to let copies already in flight land before a block that gave up ends.
 // Returns false if about `budget` clocks pass first.
