@@ -244,14 +244,36 @@ struct Line {
   int acc;                  // rows of an accumulator: a tile of more takes two
 };
 
-// First place of CTA c's share when `ctas` of them divide `tiles` tiles.
-__device__ __forceinline__ Place share_border(int64_t tiles, int nkt, int ctas, int c) {
-  if (c >= ctas) return {static_cast<int>(tiles), 0};
-  const int64_t b = tiles * nkt * c / ctas;
-  int tile = static_cast<int>(b / nkt), kt = static_cast<int>(b - static_cast<int64_t>(tile) * nkt);
+// Cost of a step of a tile of n rows: a part that does not depend on n (W is
+// decoded) and one that does.  Measured (ns): 500 + 1.5 n with books in shared
+// memory, 700 + 2.1 n with a 2^16 book, about the same proportion.
+__host__ __device__ constexpr int step_cost(int n) { return 330 + n; }
+
+// Rows of a token tile of an expert with `count` rows in `tt` tiles.
+__device__ __forceinline__ int tile_rows(int count, int tt) { return ((count + tt - 1) / tt + 15) / 16 * 16; }
+
+// First place of CTA c's share: the line cut into `ctas` parts of equal cost.
+// cost[e]: what the token tiles before expert e cost, per row tile and step.
+__device__ __forceinline__ Place share_border(const Line& l, const int64_t* cost, int ctas, int c) {
+  const int tiles = l.first[l.experts] * l.row_tiles;
+  if (c >= ctas) return {tiles, 0};
+  const int64_t per_step = cost[l.experts] * l.row_tiles;          // all tiles' cost for one step each
+  const int64_t at = static_cast<int64_t>(static_cast<double>(per_step) * l.nkt / ctas * c);
+  const int64_t unit = static_cast<int64_t>(l.row_tiles) * l.nkt;  // cost[e] counts this often
+  int lo = 0, hi = l.experts - 1;                                  // the expert the place falls into
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (cost[mid] * unit <= at) lo = mid;
+    else hi = mid - 1;
+  }
+  const int tt = l.first[lo + 1] - l.first[lo];
+  if (tt == 0) return {l.first[lo] * l.row_tiles, 0};
+  const int64_t step = (at - cost[lo] * unit) / step_cost(tile_rows(l.off[lo + 1] - l.off[lo], tt));
+  int tile = static_cast<int>(step / l.nkt), kt = static_cast<int>(step - static_cast<int64_t>(tile) * l.nkt);
   if (kt < kSnap) kt = 0;
-  else if (nkt - kt < kSnap) ++tile, kt = 0;
-  return {tile, kt};
+  else if (l.nkt - kt < kSnap) ++tile, kt = 0;
+  if (tile >= tt * l.row_tiles) tile = tt * l.row_tiles, kt = 0;
+  return {l.first[lo] * l.row_tiles + tile, kt};
 }
 
 // One CTA's part of one tile: from `at` to the tile's end or `end`, where it
@@ -279,7 +301,7 @@ struct Part {
     const int in = tile - l.first[lo] * l.row_tiles;           // row tile major
     const int rt = in / tt, j = in - rt * tt;
     const int count = l.off[lo + 1] - l.off[lo];
-    const int per = ((count + tt - 1) / tt + 15) / 16 * 16;
+    const int per = tile_rows(count, tt);
     row0 = rt * kRowTile;
     r0 = l.off[lo] + j * per;
     live = min(per, count - j * per);
@@ -481,7 +503,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   volatile int* abort_flag = &ctrl->abort;
   int* s_off = reinterpret_cast<int*>(books + g.off_table);    // [experts + 1] borders
   int* s_first = s_off + n_experts + 1;                        // [experts + 1] token tiles in front
-  Place* s_border = reinterpret_cast<Place*>(s_first + n_experts + 1);   // [CTAs + 1]
+  int64_t* s_cost = reinterpret_cast<int64_t*>(s_first + n_experts + 1);  // [experts + 1] see share_border
+  Place* s_border = reinterpret_cast<Place*>(s_cost + n_experts + 1);     // [CTAs + 1]
   float2* s_scales = reinterpret_cast<float2*>(books + g.off_scales);    // [2][tokens]
 
   if (threadIdx.x == 0) {
@@ -521,30 +544,37 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int k = k0; k < k1; ++k) s_off[k] = top = max(top, s_off[k]);
     __syncwarp();
     int sum = 0;
-    for (int k = k0; k < min(k1, n_experts); ++k) sum += (s_off[k + 1] - s_off[k] + g.tokens - 1) / g.tokens;
+    int64_t cost = 0;
+    for (int k = k0; k < min(k1, n_experts); ++k) {
+      const int count = s_off[k + 1] - s_off[k], tt = (count + g.tokens - 1) / g.tokens;
+      sum += tt;
+      if (tt) cost += static_cast<int64_t>(tt) * step_cost(tile_rows(count, tt));
+    }
     int incl = sum;
+    int64_t cincl = cost;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int v = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += v;
+      const int64_t w = __shfl_up_sync(0xffffffffu, cincl, o);
+      if (lane >= o) {
+        incl += v;
+        cincl += w;
+      }
     }
     sum = incl - sum;
+    cost = cincl - cost;
     for (int k = k0; k < k1; ++k) {
       s_first[k] = sum;
-      if (k < n_experts) sum += (s_off[k + 1] - s_off[k] + g.tokens - 1) / g.tokens;
+      s_cost[k] = cost;
+      if (k == n_experts) break;
+      const int count = s_off[k + 1] - s_off[k], tt = (count + g.tokens - 1) / g.tokens;
+      sum += tt;
+      if (tt) cost += static_cast<int64_t>(tt) * step_cost(tile_rows(count, tt));
     }
   }
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = uniform(ctrl->tmem);
-  {
-    const int64_t tiles = static_cast<int64_t>(s_first[n_experts]) * g.row_tiles;
-    const int ctas = static_cast<int>(
-        max(static_cast<int64_t>(1), min(static_cast<int64_t>(gridDim.x), tiles * g.nkt / kMinSteps)));
-    for (int c = threadIdx.x; c <= static_cast<int>(gridDim.x); c += kThreads)
-      s_border[c] = share_border(tiles, g.nkt, ctas, c);
-  }
-  __syncthreads();
   Line line;
   line.off = s_off;
   line.first = s_first;
@@ -553,6 +583,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   line.row_tiles = g.row_tiles;
   line.nkt = g.nkt;
   line.acc = kAcc;
+  {
+    const int64_t steps = static_cast<int64_t>(s_first[n_experts]) * g.row_tiles * g.nkt;
+    const int ctas = static_cast<int>(
+        max(static_cast<int64_t>(1), min(static_cast<int64_t>(gridDim.x), steps / kMinSteps)));
+    for (int c = threadIdx.x; c <= static_cast<int>(gridDim.x); c += kThreads)
+      s_border[c] = share_border(line, s_cost, ctas, c);
+  }
+  __syncthreads();
   const int cta = blockIdx.x;
   const Place from = s_border[cta], to = s_border[cta + 1];
   const int nbuf = g.tokens <= kAcc ? 2 : 1;         // accumulators in turn
@@ -753,28 +791,37 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int n0 = t.half_rows(0);
       // a shared tile: the sums to this CTA's slot (1: it starts the tile, 0: it goes on with it)
       float* mine = g.part + (2 * static_cast<int64_t>(cta) + (t.kt0 == 0 ? 1 : 0)) * slot_size + r;
+      // rows c .. c + 15 start at tensor-memory column c, or kAcc + c - n0 in the
+      // second half; the next ones are read while these are stored
+      auto read16 = [&](int c, uint32_t (&acc)[16]) { tmem_ld16(acc0 + (c < n0 ? c : kAcc + c - n0), acc); };
+      auto was_read = [&](int c) {                               // rows up to c: maybe the end of a half
+        if (c != t.n && !(nbuf == 1 && c == n0)) return;
+        tc_fence_before();
+        __syncwarp();
+        if (lane != 0) return;
+        if (nbuf == 2) mbar_arrive(&ctrl->acce[buf]);
+        if (nbuf == 1 && c == n0) mbar_arrive(&ctrl->acce[0]);
+        if (nbuf == 1 && c == t.n) mbar_arrive(&ctrl->acce[1]);
+      };
+      uint32_t acc[16];
+      read16(0, acc);
+      tmem_wait_ld();
+      was_read(16);
       for (int c = 0; c < t.n; c += 16) {
-        uint32_t acc[16];
-        // rows c .. c + 15 start at tensor-memory column c, or kAcc + c - n0 in the second half
-        tmem_ld16(acc0 + (c < n0 ? c : kAcc + c - n0), acc);
-        tmem_wait_ld();
-        if (c + 16 == t.n || (nbuf == 1 && c + 16 == n0)) {      // a half is read
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) {
-            if (nbuf == 2) mbar_arrive(&ctrl->acce[buf]);
-            if (nbuf == 1 && c + 16 == n0) mbar_arrive(&ctrl->acce[0]);
-            if (nbuf == 1 && c + 16 == t.n) mbar_arrive(&ctrl->acce[1]);
-          }
-        }
         float v[16];
 #pragma unroll
         for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(acc[i]);
+        const bool more = c + 16 < t.n;
+        if (more) read16(c + 16, acc);
         if (whole) {
           store16(v, c);
         } else {
 #pragma unroll
           for (int i = 0; i < 16; ++i) __stcg(mine + (c + i) * kRowTile, v[i]);
+        }
+        if (more) {
+          tmem_wait_ld();
+          was_read(c + 32);
         }
       }
       if (whole) continue;
@@ -1072,7 +1119,7 @@ bool fit(const Experts& E, int m, int staged, int copies, int tokens, Plan* p) {
     if (staged & (1 << b)) off += ((1 << L.b[b]) * 16 * ch) << ((copies >> b) & 1 ? 3 : 0);
   }
   p->off_table = off;
-  off += 8 * (E.e + 1) + 8 * (device_sm_count() + 1);
+  off += 16 * (E.e + 1) + 8 * (device_sm_count() + 1);
   p->off_scales = off = (off + 15) / 16 * 16;
   off += 2 * 8 * std::min((m + 15) / 16 * 16, tokens);
   const int room = device_smem_optin() - 2048 - off;
@@ -1083,7 +1130,9 @@ bool fit(const Experts& E, int m, int staged, int copies, int tokens, Plan* p) {
   if (p->tokens <= acc) {
     p->na = kMaxA;
     for (p->xk = 4; p->xk > 1 && (room - p->na * atile) / (slot * p->xk) < 2; p->xk /= 2) {}
-    p->nx = std::min(kMaxX, (room - p->na * atile) / (slot * p->xk));
+    // three slots of several steps are enough to stay ahead; what is left serves
+    // the index words as L1
+    p->nx = std::min(p->xk > 1 ? 3 : kMaxX, (room - p->na * atile) / (slot * p->xk));
     if (p->nx < (p->xk > 1 ? 2 : 3)) return false;
   } else {
     p->xk = 1;

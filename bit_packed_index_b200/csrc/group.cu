@@ -44,8 +44,24 @@ size_t group_smem(int n_experts) {
   return (static_cast<size_t>(kGroupWarps + 3) * n_experts + 64) * sizeof(int);
 }
 
+// n / d for n < 2^30 (d >= 1) as a multiplication.
+struct Divisor {
+  uint32_t mul;
+  int shift;
+};
+Divisor divisor(uint32_t d) {
+  int s = 0;
+  while ((1u << s) < d) ++s;
+  return {static_cast<uint32_t>((((1ull << s) - d) << 32) / d + 1), s};
+}
+__device__ __forceinline__ int quotient(int n, Divisor d) {
+  return static_cast<int>((__umulhi(static_cast<uint32_t>(n), d.mul) + static_cast<uint32_t>(n)) >> d.shift);
+}
+
+constexpr int kHeld = 8;      // passes of a run whose ids stay in registers between counting and placing
+
 __global__ void __launch_bounds__(kGroupThreads) group_rows_kernel(const int32_t* __restrict__ ids, int n_tokens,
-                                                                  int top_k, int64_t ld_ids, int n_experts,
+                                                                  int top_k, Divisor by_k, int64_t ld_ids, int n_experts,
                                                                   int32_t* __restrict__ offsets,
                                                                   int32_t* __restrict__ rows,
                                                                   int32_t* __restrict__ pos) {
@@ -60,15 +76,32 @@ __global__ void __launch_bounds__(kGroupThreads) group_rows_kernel(const int32_t
   const int picks = n_tokens * top_k;
   const int nw = nc * kGroupWarps;
   const int run = (picks + nw * 32 - 1) / (nw * 32) * 32;   // picks of a warp, a multiple of 32
-  const int p0 = min(static_cast<int64_t>(picks), static_cast<int64_t>(c * kGroupWarps + warp) * run);
-  const int p1 = min(static_cast<int64_t>(picks), static_cast<int64_t>(p0) + run);
+  const int p0 = static_cast<int>(min(static_cast<int64_t>(picks), static_cast<int64_t>(c * kGroupWarps + warp) * run));
+  const int p1 = static_cast<int>(min(static_cast<int64_t>(picks), static_cast<int64_t>(p0) + run));
+  int* mine = hist + warp * n_experts;
 
+  // the id of pick p, or -1 where it names no expert (or there is no pick p)
+  auto load = [&](int p) {
+    if (p >= p1) return -1;
+    int64_t at = p;
+    if (ld_ids != top_k) {
+      const int t = quotient(p, by_k);
+      at = t * ld_ids + (p - t * top_k);
+    }
+    const int id = __ldg(ids + at);
+    return id >= 0 && id < n_experts ? id : -1;
+  };
+  int held[kHeld];
+#pragma unroll
+  for (int i = 0; i < kHeld; ++i) held[i] = load(p0 + 32 * i + lane);
   for (int i = tid; i < kGroupWarps * n_experts; i += kGroupThreads) hist[i] = 0;
   __syncthreads();
-  for (int p = p0 + lane; p < p1; p += 32) {
-    const int t = p / top_k;
-    const int id = __ldg(ids + t * ld_ids + (p - t * top_k));
-    if (id >= 0 && id < n_experts) atomicAdd(&hist[warp * n_experts + id], 1);
+#pragma unroll
+  for (int i = 0; i < kHeld; ++i)
+    if (held[i] >= 0) atomicAdd(&mine[held[i]], 1);
+  for (int p = p0 + 32 * kHeld + lane; p < p1; p += 32) {
+    const int id = load(p);
+    if (id >= 0) atomicAdd(&mine[id], 1);
   }
   __syncthreads();
   if (tid < n_experts) {                               // exclusive over the warps
@@ -84,6 +117,7 @@ __global__ void __launch_bounds__(kGroupThreads) group_rows_kernel(const int32_t
   cluster.sync();
   int all = 0, below = 0;
   if (tid < n_experts) {
+#pragma unroll 8
     for (int k = 0; k < nc; ++k) {
       const int v = *cluster.map_shared_rank(total + tid, k);
       below += k < c ? v : 0;
@@ -119,24 +153,24 @@ __global__ void __launch_bounds__(kGroupThreads) group_rows_kernel(const int32_t
   const int n_rows = scan[32];
   if (c == 0 && tid == 0) offsets[n_experts] = n_rows;
   cluster.sync();                                      // `first` is set, and no CTA leaves while others read `total`
-  for (int q = p0; q < p1; q += 32) {
-    const int p = q + lane;
-    const bool in = p < p1;
-    int t = 0, id = -1;
-    if (in) {
-      t = p / top_k;
-      id = __ldg(ids + t * ld_ids + (p - t * top_k));
-    }
-    const bool ok = in && id >= 0 && id < n_experts;
-    const uint32_t same = __match_any_sync(0xffffffffu, ok ? id : -1);
+  // 32 picks in order: every pick's row is the expert's next one plus the lower
+  // lanes with the same expert; the highest of them moves the expert on
+  auto place = [&](int p, int id) {
+    const uint32_t same = __match_any_sync(0xffffffffu, id);
     int r = -1;
-    if (ok) r = first[id] + hist[warp * n_experts + id] + __popc(same & ((1u << lane) - 1u));
+    if (id >= 0) r = first[id] + mine[id] + __popc(same & ((1u << lane) - 1u));
     __syncwarp();
-    if (ok && (same >> lane) == 1u) hist[warp * n_experts + id] += __popc(same);   // the highest lane of each expert
+    if (id >= 0 && (same >> lane) == 1u) mine[id] += __popc(same);
     __syncwarp();
-    if (ok) rows[r] = t;
-    if (in) pos[p] = r;
-  }
+    if (p < p1) {
+      pos[p] = r;
+      if (id >= 0) rows[r] = quotient(p, by_k);
+    }
+  };
+#pragma unroll
+  for (int i = 0; i < kHeld; ++i)
+    if (p0 + 32 * i < p1) place(p0 + 32 * i + lane, held[i]);
+  for (int q = p0 + 32 * kHeld; q < p1; q += 32) place(q + lane, load(q + lane));
   for (int64_t i = n_rows + static_cast<int64_t>(c) * kGroupThreads + tid; i < picks; i += static_cast<int64_t>(nc) * kGroupThreads)
     rows[i] = -1;
 }
@@ -311,8 +345,8 @@ vq_status vq_group_rows(const int32_t* ids, int32_t n_tokens, int32_t top_k, int
   cfg.numAttrs = 1;
   count_launch();
   return cuda_status(cudaLaunchKernelEx(&cfg, group_rows_kernel, ids, static_cast<int>(n_tokens),
-                                        static_cast<int>(top_k), ld_ids, static_cast<int>(n_experts), offsets, rows,
-                                        pos));
+                                        static_cast<int>(top_k), divisor(static_cast<uint32_t>(top_k)), ld_ids,
+                                        static_cast<int>(n_experts), offsets, rows, pos));
 }
 
 vq_status vq_combine_rows(const void* z, vq_dtype z_dtype, int32_t z_rows, int32_t n, int64_t ldz, const int32_t* pos,
