@@ -2,7 +2,7 @@
 // order of their experts, and the experts' results added up per token.
 //
 // Grouping is a stable counting sort, pos(p) = #{picks of smaller experts} +
-// #{earlier picks of the same expert}, in one launch: a cluster of up to eight
+// #{earlier picks of the same expert}, in one launch: a cluster of up to sixteen
 // CTAs shares the picks, each warp owning a run of consecutive ones.
 //   1. every warp counts its run into a histogram of its own (shared memory);
 //   2. a scan over the warps, the CTAs (their totals through distributed
@@ -15,8 +15,11 @@
 //
 // Combining reads every picked row once and writes every token once (HBM is
 // the bound for a prefill chunk); a thread owns eight columns of a token and
-// issues the loads of all its picks before the first sum.
+// issues the loads of several picks before the first sum, past the caches'
+// keeping (each row is read once).
 #include <algorithm>
+#include <mutex>
+#include <vector>
 
 #include <cooperative_groups.h>
 
@@ -30,15 +33,6 @@ namespace cg = cooperative_groups;
 
 constexpr int kGroupThreads = 1024;
 constexpr int kGroupWarps = kGroupThreads / 32;
-
-// One pick per thread and pass is the least a CTA can do; more CTAs pay once
-// a warp's run is longer than a few passes (the two cluster barriers cost
-// about as much as two passes).
-int group_ctas(int64_t picks) {
-  int c = 1;
-  while (c < 8 && picks > static_cast<int64_t>(c) * kGroupThreads * 2) c *= 2;
-  return c;
-}
 
 size_t group_smem(int n_experts) {
   return (static_cast<size_t>(kGroupWarps + 3) * n_experts + 64) * sizeof(int);
@@ -180,7 +174,7 @@ struct Load8;   // eight consecutive values as fp32
 template <>
 struct Load8<__half> {
   uint4 u;
-  __device__ __forceinline__ void load(const void* p) { u = __ldg(reinterpret_cast<const uint4*>(p)); }
+  __device__ __forceinline__ void load(const void* p) { u = __ldcs(reinterpret_cast<const uint4*>(p)); }
   __device__ __forceinline__ void get(float (&v)[8]) const {
     const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
@@ -193,7 +187,7 @@ struct Load8<__half> {
 template <>
 struct Load8<__nv_bfloat16> {
   uint4 u;
-  __device__ __forceinline__ void load(const void* p) { u = __ldg(reinterpret_cast<const uint4*>(p)); }
+  __device__ __forceinline__ void load(const void* p) { u = __ldcs(reinterpret_cast<const uint4*>(p)); }
   __device__ __forceinline__ void get(float (&v)[8]) const {
     const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
@@ -207,8 +201,8 @@ template <>
 struct Load8<float> {
   float4 a, b;
   __device__ __forceinline__ void load(const void* p) {
-    a = __ldg(reinterpret_cast<const float4*>(p));
-    b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+    a = __ldcs(reinterpret_cast<const float4*>(p));
+    b = __ldcs(reinterpret_cast<const float4*>(p) + 1);
   }
   __device__ __forceinline__ void get(float (&v)[8]) const {
     v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
@@ -224,12 +218,16 @@ __device__ __forceinline__ float load1(const void* p, int64_t i) {
 }
 
 constexpr int kCombineThreads = 256;
-constexpr int kCombineAhead = 8;     // picks whose loads are in flight together
+// Picks whose loads are in flight together, and blocks per SM.  8192 tokens x 8
+// picks x 4096 columns: 8 and 2 took 124 us, 8 and 4 110, 4 and 6 123, 4 and 5
+// 99 us (6.1 TB/s); 2048 x 2 x 8192: 49, 40, 33, 24 us.
+constexpr int kCombineAhead = 4;
+constexpr int kCombineBlocks = 5;
 
 // One group of eight columns of a token per thread; VEC: rows of z (and y)
 // start on 16 bytes, so whole groups move as 16-byte words.
 template <typename T, bool VEC>
-__global__ void __launch_bounds__(kCombineThreads) combine_rows_kernel(
+__global__ void __launch_bounds__(kCombineThreads, kCombineBlocks) combine_rows_kernel(
     const T* __restrict__ z, int z_rows, int n, int64_t ldz, const int32_t* __restrict__ pos,
     const float* __restrict__ weight, int64_t ld_weight, int n_tokens, int top_k, void* __restrict__ y, vq_dtype yt,
     int64_t ldy) {
@@ -309,6 +307,56 @@ cudaError_t launch_combine(bool vec, const void* z, int z_rows, int n, int64_t l
   return cudaGetLastError();
 }
 
+// Whether a cluster of sixteen CTAs with this much shared memory fits the
+// current device (remembered per device for the largest size asked).
+bool wide_clusters(size_t smem) {
+  struct Entry {
+    int dev;
+    size_t smem;
+    bool ok;
+  };
+  static std::mutex mu;
+  static std::vector<Entry> known;
+  int dev = 0;
+  cudaGetDevice(&dev);
+  {
+    std::lock_guard<std::mutex> lock(mu);
+    for (const Entry& e : known)
+      if (e.dev == dev && e.smem == smem) return e.ok;
+  }
+  const void* k = reinterpret_cast<const void*>(group_rows_kernel);
+  bool ok = set_func_attr(k, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess;
+  if (ok) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(16);
+    cfg.blockDim = dim3(kGroupThreads);
+    cfg.dynamicSmemBytes = smem;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 16;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    ok = cudaOccupancyMaxActiveClusters(&n, group_rows_kernel, &cfg) == cudaSuccess && n > 0;
+    if (!ok) cudaGetLastError();   // leave no error for the launch to report
+  }
+  std::lock_guard<std::mutex> lock(mu);
+  known.push_back({dev, smem, ok});
+  return ok;
+}
+
+// One pick per thread and pass is the least a CTA can do; more CTAs pay once
+// a warp's run is longer than a few passes (the two cluster barriers cost
+// about as much as two passes).
+// Sixteen CTAs (more than a portable cluster) halve the time of long runs,
+// which scattered stores bound, where the device can place them.
+int group_ctas(int64_t picks, size_t smem) {
+  int c = 1;
+  while (c < 16 && picks > static_cast<int64_t>(c) * kGroupThreads * 2) c *= 2;
+  return c == 16 && !wide_clusters(smem) ? 8 : c;
+}
+
 bool float_type(vq_dtype t) { return t == VQ_BF16 || t == VQ_FP16 || t == VQ_FP32; }
 size_t type_size(vq_dtype t) { return t == VQ_FP32 ? 4 : 2; }
 
@@ -331,7 +379,7 @@ vq_status vq_group_rows(const int32_t* ids, int32_t n_tokens, int32_t top_k, int
   cudaError_t e = set_func_attr(reinterpret_cast<const void*>(group_rows_kernel),
                                 cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
   if (e != cudaSuccess) return cuda_status(e);
-  const int nc = group_ctas(picks);
+  const int nc = group_ctas(picks, smem);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(nc);
   cfg.blockDim = dim3(kGroupThreads);
