@@ -130,22 +130,34 @@ __global__ void __launch_bounds__(kPrepThreads) experts_prep_kernel(
 
 // ---------------------------------------------------------------------------
 // The product.  y^T = W_e x'^T per expert: 128 rows of W are the MMA's M, up to
-// 512 rows of the group its N (two products of at most 256), so that a decoding
-// step's one row and a prompt's hundreds take the same path and W is decoded
-// once per 512 rows.
+// 384 rows of the group (512 where W's tiles lie in shared memory) its N, in two
+// halves, so that a decoding step's one row and a prompt's hundreds take the
+// same path and W is decoded once per 384 or 512 rows.
+//
+// What bounds it, per step of 128 x 64 weights (1024 vectors of eight), in
+// clocks of the SM: the lookups of two staged books, 333 + 128 shared-memory
+// wavefronts (16-byte rows of a 2^12 book at random, 2.6 lanes of a phase on a
+// bank; the residual's eight copies meet none); for n rows n more to write x'
+// and n to read it, and 2 n of tensor time.  So few rows cost what the lookups
+// cost, 384 rows 1230 clocks of shared memory against 768 of products.  A 2^16
+// book costs 1024 gathers at the 0.84 a clock that L2 hands out, 1220 clocks.
+// Measured (B200, 148 SMs, weights cold): two 14336 x 4096 experts of 12 + 8 bits
+// for one row 53 us (0.35 us a step, 20 us before the first and after the last);
+// eight of them for 8192 rows 1.02 ms, 943 TFLOP/s (1.2 ms under the power cap);
+// sixteen 4096 x 2048 experts with 2^16 books for 62 rows each 99 us.
 //
 //  * Sixteen producer warps decode W.  They work in four groups of 128 threads,
 //    group i taking every fourth step (64 columns) from the i-th on; a thread
 //    owns one row of the tile: it reads the row's index fields of the step
 //    (loaded one turn ahead), gathers the centroids (small books staged in
 //    shared memory, large ones through L2), adds the two books' and writes the
-//    128-byte-swizzled row.  Whole steps per group keep the per-step cost (a
+//    row of the tile.  Whole steps per group keep the per-step cost (a
 //    barrier, the addresses) at a quarter of what it is when all warps share
 //    each step, and the other groups' steps hide a group's gather latency.
-//  * x' arrives by TMA in a ring of its own; one thread issues tcgen05.mma;
-//    four warps read the accumulators back and store y.
+//  * x' arrives by TMA in a ring of its own; one warp issues tcgen05.mma; four
+//    warps read the accumulators back and store y.
 //  * The work of all groups is one line of (expert, row tile, token tile,
-//    step), cut into equal shares, one per CTA, whatever the group sizes.  A
+//    step), cut into shares of equal cost, one per CTA, whatever the group sizes.  A
 //    tile that two or more CTAs share is joined through the workspace: each
 //    writes its partial sums, and the one that arrives last adds them in the
 //    order of the shares (no wait, and the same order every time).
@@ -406,8 +418,9 @@ __device__ __forceinline__ uint32_t any_field(const Layer& L, int m, int64_t o, 
                                  : load_field(L.idx[m] + (j >> 2) * L.rw[m], (4 * o + (j & 3)) * b, b);
 }
 
-// x' comes in boxes of kBoxes rows by xk steps, one box for a tile's half: a
-// load's issue takes its thread longer than most boxes take to arrive.
+// x' comes in boxes of box_rows() rows by xk steps, one box for a tile's half: a
+// load's issue takes its warp about 450 clocks, whatever the box holds, longer
+// than the other warps take for a step of few rows.
 constexpr int kBoxes = 5;
 __host__ __device__ constexpr int box_rows(int i, int acc) { return i < 4 ? 16 << i : acc; }
 __host__ __device__ constexpr int box_of(int n) { return n <= 16 ? 0 : n <= 32 ? 1 : n <= 64 ? 2 : n <= 128 ? 3 : 4; }

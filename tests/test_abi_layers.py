@@ -127,6 +127,7 @@ def test_gemm_experts_refusals(lib):
     for bad in (dict(x=0x1001), dict(rows=0x2002), dict(off=0x3002), dict(y=0x4001), dict(ws=0x5010)):
         assert call(**bad) == ALIGN, bad
     assert call(m=(1 << 24) + 1) == UNSUPPORTED
+    assert call(D=_ex(n=1 << 30), m=1 << 20, xr=1 << 20, ldy=1 << 30) == UNSUPPORTED      # tiles past 2^31
     assert call(ws=None) == WORKSPACE
     assert call(nws=128) == WORKSPACE
     assert call(m=0, x=None, y=None, ws=None) == OK

@@ -197,6 +197,53 @@ def test_long_and_empty_groups(counts):
     _check(_run(ex, x, offsets), x, data, offsets, None, -3.0)
 
 
+@pytest.mark.parametrize("books,layout", [((12, 8), "rows"), ((16,), "tile4"), ((16, 8), "rows"), ((9, 9), "tile4")])
+@pytest.mark.parametrize("counts", [[1, 2000, 0, 7, 130, 0, 385, 193], [600, 520]])
+def test_uneven_groups(books, layout, counts):
+    """One expert with most of the rows: token tiles of one and two halves, and
+    shares that end inside tiles, in both places that W's tiles can lie."""
+    spec = LayerSpec(400, 328, 8, books, (0.02, 0.005)[: len(books)])
+    data, ex = _experts(spec, len(counts), layout, 13)
+    x = torch.randn((sum(counts) + 3, 328), device="cuda").bfloat16()
+    y = _run(ex, x, _offsets(counts), od=torch.bfloat16)
+    _check(y, x, data, _offsets(counts), None, -3.0)
+
+
+def test_many_experts_many_rows():
+    """1024 experts, the most, each with its own small books."""
+    spec = LayerSpec(130, 48, 8, (5, 3), (0.02, 0.005))
+    data, ex = _experts(spec, 1024, "tile4", 100)
+    rng = np.random.default_rng(0)
+    counts = rng.integers(0, 6, size=1024)
+    counts[500] = 100
+    x = torch.randn((int(counts.sum()), 48), device="cuda").half()
+    _check(_run(ex, x, _offsets(counts)), x, data, _offsets(counts), None, -3.0)
+
+
+def test_one_workspace_for_two_graphs():
+    """Two captured calls that share a workspace, replayed one after the other."""
+    vq = _vq()
+    data, ex = _experts(LayerSpec(700, 500, 8, (12, 8), (0.02, 0.005)), 3, "tile4", 41)
+    xs = [torch.randn((m, 500), device="cuda").bfloat16() for m in (5, 300)]
+    offs = [_offsets([2, 0, 3]), _offsets([100, 150, 50])]
+    ys = [torch.empty((x.shape[0], 700), dtype=torch.float32, device="cuda") for x in xs]
+    work = torch.zeros(max(vq.gemm_experts_workspace_size(ex, x.shape[0]) for x in xs), dtype=torch.uint8, device="cuda")
+    graphs = []
+    for x, o, y in zip(xs, offs, ys):
+        vq.gemm_experts(ex, x, o, out=y, workspace=work)
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            vq.gemm_experts(ex, x, o, out=y, workspace=work)
+    for _ in range(3):
+        for x in xs:
+            x.copy_(torch.randn_like(x))
+        for g in graphs:
+            g.replay()
+        torch.cuda.synchronize()
+        for x, o, y in zip(xs, offs, ys):
+            _check(y, x, data, o, None, -3.0)
+
+
 def test_many_experts_few_rows():
     spec = LayerSpec(128, 96, 8, (6, 4), (0.02, 0.005))
     data, ex = _experts(spec, 200, "rows", 11)
