@@ -1103,6 +1103,12 @@ struct Plan {
   size_t off_xe, off_sum, off_joined, off_xh, off_part, total;
 };
 
+// A token tile holds so many times the rows that the experts have on average: an
+// expert above it is decoded twice, a larger tile leaves fewer x slots and less
+// L1.  Routed unevenly (the most popular of 16 or 64 experts at two to three
+// times the average), 2, 3 and 4 took 131 / 119 / 119 us (1000 x 2 of 16, 12 + 8
+// bits), 239 / 229 / 237 (2000 x 2 of 16, 16 + 8) and 158 / 149 / 172 (512 x 8 of 64).
+constexpr int kSpread = 3;
 constexpr int kMaxCopied = 8;      // log2 entries of a book that may be kept eight times (32 KB at d <= 8)
 
 // The kernel that serves a layer with the books of mask `staged` in shared
@@ -1173,7 +1179,7 @@ Plan plan_experts(const Experts& E, int m) {
   // of more than 2^13 entries never fits), then the token tile (W is decoded once
   // per token tile), then eight copies of small books (their lookups meet no bank
   // conflicts).  The tile: the smallest of 64, 128, one and two accumulators that
-  // holds twice the rows that the experts have on average, so that few are cut.
+  // holds kSpread times the rows that the experts have on average.
   const int both = L.nb == 2 ? 3 : 1;
   int small = 0;
   for (int b = 0; b < L.nb; ++b) small |= L.b[b] <= kMaxCopied ? 1 << b : 0;
@@ -1185,7 +1191,7 @@ Plan plan_experts(const Experts& E, int m) {
     const int acc = acc_rows(w_in_tmem(widths_of(L, mask).b1));
     const int sizes[5] = {2 * acc, acc, 128, 64, 32};
     int first = 3;
-    while (first > 0 && static_cast<int64_t>(sizes[first]) * E.e < 2 * static_cast<int64_t>(m)) --first;
+    while (first > 0 && static_cast<int64_t>(sizes[first]) * E.e < kSpread * static_cast<int64_t>(m)) --first;
     for (int i = first; i < 5; ++i)
       for (int copies : {mask & small, mask & small & 2, 0})
         if (!done && fit(E, m, mask, copies, sizes[i], &p)) done = true;

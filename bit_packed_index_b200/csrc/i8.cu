@@ -204,7 +204,7 @@ constexpr int kRows = 128;                 // output channels per CTA
 constexpr int kStepBytes = 128;            // values of k per step
 constexpr int kWTile = kRows * kStepBytes;
 constexpr int kMaxStages = 8;
-constexpr int kCtrlBytes = 3072;           // control block in front of the stages (a multiple of 1024)
+constexpr int kCtrlBytes = 3 * 1024;       // control block in front of the stages (a multiple of 1024)
 constexpr long long kDrain = 1LL << 26;    // SM clocks: far above any load's latency
 
 __device__ __forceinline__ uint8_t* align1024(uint8_t* p) {
@@ -245,7 +245,7 @@ __device__ __forceinline__ void store_rows(vq_dtype yt, uint8_t* yo, int64_t ldb
   else store_rows<VQ_FP32>(yo, ldb, acc, n, scales, w, b);
 }
 
-// ---- one to 64 rows: W's bytes are the bound ------------------------------------
+// ---- few rows: W's bytes are the bound ------------------------------------
 // A cluster of S CTAs shares a tile of 128 outputs, each CTA a run of k, so
 // that even a layer of 1024 outputs keeps most SMs loading.  The partial sums
 // meet in distributed shared memory: integers, so the split changes nothing
@@ -254,10 +254,13 @@ struct NarrowCtrl {
   uint64_t full[kMaxStages], empty[kMaxStages], acc;
   uint32_t tmem;
   int abort;
-  alignas(16) float scales[64];            // activation scales
+  alignas(16) float scales[64];            // activation scales (kNarrowRows of them)
 };
 static_assert(sizeof(NarrowCtrl) <= kCtrlBytes, "control block");
-constexpr int kNarrowRows = 64;
+// Rows up to which this kernel runs: 8192 x 8192 from bf16 takes 18.3 us here and
+// 19.7 in the wide kernel for 24 rows, 19.6 and 20.6 for 48, 20.8 in both for 64
+// (the product alone 19.3 and 17.8).
+constexpr int kNarrowRows = 48;
 constexpr int kNarrowThreads = 192;        // warp 0: loads, warp 1: products, warps 2-5: epilogue
 
 __global__ void __launch_bounds__(kNarrowThreads) gemm_i8_narrow_kernel(const __grid_constant__ CUtensorMap wmap,
@@ -636,6 +639,9 @@ long long wait_budget() {
 
 // Splits of the narrow kernel: double the cluster while the grid stays within
 // two CTAs per SM and each CTA keeps at least four steps (512 bytes of k).
+// 24 x 8192 x 8192 with 2, 4 (chosen) and 8 CTAs a cluster: 18.0, 16.4, 19.8 us;
+// 4 x 4096 x 4096 with 4 and 8 (chosen): 5.3, 5.8; 16 x 14336 x 4096 with 1 and 2
+// (chosen): 14.1, 15.6.
 int narrow_splits(int tiles, int num_kt, int sms) {
   int s = 1;
   while (s < 8 && tiles * s * 2 <= 2 * sms && num_kt >= 8 * s) s *= 2;
@@ -644,7 +650,10 @@ int narrow_splits(int tiles, int num_kt, int sms) {
 
 // Rows per tile of the wide kernel: the multiple of 32 that takes the fewest
 // clocks over the last wave of pairs, a step costing 2 tn clocks of the tensor
-// cores or the time its 16 KB of weights and tn / 2 rows take to arrive.
+// cores or the time its 16 KB of weights and tn / 2 rows take to arrive.  With
+// 64, 128, 256 rows and the rule's choice: 333 x 4100 x 2000 13.2, 11.0, 15.4 and
+// 10.1 us (96 rows), 1000 x 2048 x 4096 14.5, 12.1, 18.8 and 12.2, 512 x 8192 x
+// 8192 44.4, 30.5, 29.5 and 29.7.
 int wide_rows(int m, int tiles_n, int pairs) {
   int best = kWideTn;
   int64_t least = -1;
