@@ -597,9 +597,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   line.nkt = g.nkt;
   line.acc = kAcc;
   {
-    const int64_t steps = static_cast<int64_t>(s_first[n_experts]) * g.row_tiles * g.nkt;
-    const int ctas = static_cast<int>(
-        max(static_cast<int64_t>(1), min(static_cast<int64_t>(gridDim.x), steps / kMinSteps)));
+    // a CTA for each tile at least, more where their steps are worth cutting
+    const int64_t tiles = static_cast<int64_t>(s_first[n_experts]) * g.row_tiles;
+    const int ctas = static_cast<int>(max(
+        static_cast<int64_t>(1), min(static_cast<int64_t>(gridDim.x), max(tiles, tiles * g.nkt / kMinSteps))));
     for (int c = threadIdx.x; c <= static_cast<int>(gridDim.x); c += kThreads)
       s_border[c] = share_border(line, s_cost, ctas, c);
   }
@@ -1192,6 +1193,11 @@ Plan plan_experts(const Experts& E, int m) {
     const int sizes[5] = {2 * acc, acc, 128, 64, 32};
     int first = 3;
     while (first > 0 && static_cast<int64_t>(sizes[first]) * E.e < kSpread * static_cast<int64_t>(m)) --first;
+    // short rows of W: smaller tiles where the steps cannot occupy every CTA
+    // (9104 rows of 161 x 66: 123 us in tiles of 512 on ten CTAs, 37 us in tiles of 64)
+    while (first < 3 && static_cast<int64_t>(p.row_tiles) * ((m + sizes[first] - 1) / sizes[first]) * p.nkt <
+                            static_cast<int64_t>(kMinSteps) * p.ctas)
+      ++first;
     for (int i = first; i < 5; ++i)
       for (int copies : {mask & small, mask & small & 2, 0})
         if (!done && fit(E, m, mask, copies, sizes[i], &p)) done = true;

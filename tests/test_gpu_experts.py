@@ -439,3 +439,13 @@ def test_binding_checks():
         vq.Experts(32, 64, 8, [9], ex.idx, ex.codebooks)
     with pytest.raises(ValueError):
         vq.Experts.from_layers([ex.layer(0), vq.repack_tile4(ex.layer(1))])
+
+
+@pytest.mark.parametrize("n,kin,books,d", [(161, 66, (16, 8), 8), (112, 96, (8,), 4), (40, 9, (12, 4), 6)])
+def test_many_rows_of_short_weights(n, kin, books, d):
+    """Few steps per tile: a tile per CTA and more, none of them cut."""
+    spec = LayerSpec(n, kin, d, books, (0.02, 0.005)[: len(books)], out_bias_std=1.0)
+    counts = [900, 0, 333, 1500]
+    data, ex = _experts(spec, 4, "rows", 17)
+    x = torch.randn((sum(counts), kin), device="cuda").bfloat16()
+    _check(_run(ex, x, _offsets(counts)), x, data, _offsets(counts), None, -3.0)
