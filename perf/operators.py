@@ -256,7 +256,7 @@ def run(state):
 
 def _linear_plain(x, w, ws, b, out):
     top = x.float().abs().amax(dim=1, keepdim=True)
-    s = top / 127.0
+    s = (top.double() / 127.0).float()      # rounded once; fp32 by a number becomes a product with 1 / 127 on the GPU
     q = torch.round(x.double() / s.double()).clamp(-127, 127).float()       # 64 bits: quotients next to a half
     y = (q @ w.float().t()) * s * ws
     return (y if b is None else y + b.float()).to(out)
