@@ -338,17 +338,19 @@ struct Words {
   static constexpr int per = LAYOUT == VQ_IDX_TILE4 ? (B == 4 ? 1 : B / 8 + (B == 12)) : B / 4;   // words of a record, of a step
   static constexpr int count = LAYOUT == VQ_IDX_TILE4 ? 2 * per : per;
   const uint32_t* base;
-  int64_t stride;           // words of a stream row / tile
+  int64_t stride;           // tiled: words of a tile; row order: words that the row's own fields take, which may be
+                            // fewer than lie between two rows (the last row need not own the rest)
   int tiles, shift;
 
   __device__ __forceinline__ void set(const Layer& L, int m, int64_t o) {
-    stride = L.rw[m];
     if constexpr (LAYOUT == VQ_IDX_TILE4) {
+      stride = L.rw[m];
       base = L.idx[m] + ((o * (4 * B)) >> 5);
       shift = static_cast<int>((o * (4 * B)) & 31);
       tiles = (L.nvec + 3) / 4;
     } else {
-      base = L.idx[m] + o * stride;
+      stride = (static_cast<int64_t>(L.nvec) * B + 127) / 128 * 4;
+      base = L.idx[m] + o * L.rw[m];
       shift = 0;
     }
   }

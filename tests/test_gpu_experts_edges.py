@@ -1,0 +1,51 @@
+"""vq_gemm_experts at its edges.  Bounds and helpers: tests/test_gpu_experts.py."""
+import numpy as np
+import pytest
+import torch
+
+import oracle
+import synth
+from synth import LayerSpec
+from tests.test_gpu_experts import _check, _experts, _offsets, _run, _vq
+
+pytestmark = pytest.mark.gpu
+
+
+# ---- index streams that are columns of a wider array --------------------------
+def _column_experts(spec, e, after, seed):
+    """Row-order experts whose index words are columns 4 .. of a wider array,
+    `after` words of ones behind them.  A field of ones names the last entry of
+    its book, an infinity that no vector uses: a read past a row's own words
+    shows as NaN (the fields behind the last vector meet zeros of x)."""
+    vq = _vq()
+    data = [synth.make_layer(spec, seed=seed + i) for i in range(e)]
+    idx, books = [], []
+    for m, b in enumerate(spec.log2k):
+        words = []
+        for d in data:
+            fields = oracle.unpack(d.idx_words[m], b, spec.nvec)
+            d.idx_words[m] = oracle.pack(np.minimum(fields, (1 << b) - 2).astype(np.uint32), b, d.idx_words[m].shape[1])
+            words.append(d.idx_words[m])
+        words = np.stack(words)
+        wide = np.full((e, spec.out_features, 4 + words.shape[2] + after), 0xFFFFFFFF, np.uint32)
+        wide[:, :, 4: 4 + words.shape[2]] = words
+        idx.append(torch.from_numpy(wide.view(np.int32)).cuda()[:, :, 4: 4 + words.shape[2]])
+        book = torch.from_numpy(np.stack([d.codebooks[m] for d in data]).view(np.int16)).cuda().view(torch.float16)
+        book = book.reshape(e, 1 << b, spec.d).clone()
+        book[:, -1] = float("inf")
+        books.append(book)
+    half = lambda name: torch.from_numpy(np.stack([getattr(d, name) for d in data]).view(np.int16)).cuda().view(torch.float16)
+    return data, vq.Experts(spec.out_features, spec.in_features, spec.d, list(spec.log2k), idx, books, half("scale"),
+                            half("bias"))
+
+
+@pytest.mark.parametrize("after", [4, 0], ids=["inside", "at_the_end"])
+@pytest.mark.parametrize("books", [(12, 8), (12, 4), (12,), (16,), (8, 8)])
+@pytest.mark.parametrize("nvec", [9, 10, 17, 21, 41, 50])
+def test_index_words_in_columns_of_a_wider_array(nvec, books, after):
+    """`inside`: words follow each row; `at_the_end`: the last row of the last
+    expert ends with the storage."""
+    spec = LayerSpec(130, 8 * nvec - 3, 8, books, (0.02, 0.005)[: len(books)])
+    data, ex = _column_experts(spec, 2, after, 3 * nvec)
+    x = torch.randn((21, spec.in_features), device="cuda").bfloat16()
+    _check(_run(ex, x, _offsets([2, 17])), x, data, _offsets([2, 17]), None, -3.0)
