@@ -718,7 +718,8 @@ class Experts:
     ``codebooks[m]`` float16 [E][K][d] or [1][K][d] (one book for all), scale,
     bias and out_bias float16 [E][N] or [1][N].  ``from_layers`` stacks
     ``Layer`` objects; ``layer(e)`` is expert e as a ``Layer`` on the same
-    memory."""
+    memory (index words that are columns of a wider array are copied: a layer's
+    last row has to own the whole distance between two rows)."""
 
     def __init__(self, out_features: int, in_features: int, vec_dim: int, log2k: Sequence[int],
                  idx: Sequence[torch.Tensor], codebooks: Sequence[torch.Tensor], scale: Optional[torch.Tensor] = None,
@@ -790,7 +791,8 @@ class Experts:
 
     def layer(self, e: int) -> Layer:
         at = lambda t: None if t is None else t[e if t.shape[0] > 1 else 0]
-        return Layer(self.out_features, self.in_features, self.vec_dim, list(self.log2k), [t[e] for t in self.idx],
+        whole = lambda t: t if t.stride(0) == t.shape[1] else t.clone(memory_format=torch.contiguous_format)
+        return Layer(self.out_features, self.in_features, self.vec_dim, list(self.log2k), [whole(t[e]) for t in self.idx],
                      [at(c) for c in self.codebooks], at(self.scale), at(self.bias), layout=self.layout,
                      out_bias=at(self.out_bias))
 

@@ -49,3 +49,16 @@ def test_index_words_in_columns_of_a_wider_array(nvec, books, after):
     data, ex = _column_experts(spec, 2, after, 3 * nvec)
     x = torch.randn((21, spec.in_features), device="cuda").bfloat16()
     _check(_run(ex, x, _offsets([2, 17])), x, data, _offsets([2, 17]), None, -3.0)
+
+
+@pytest.mark.parametrize("n", [130, 1])
+def test_one_of_those_experts_as_a_layer(n):
+    """A layer's arrays own the distance between rows behind the last row too."""
+    spec = LayerSpec(n, 8 * 17, 8, (12, 8), (0.02, 0.005))
+    data, ex = _column_experts(spec, 2, 0, 5)
+    x = torch.randn((3, spec.in_features), device="cuda").bfloat16()
+    for e in range(2):
+        layer = ex.layer(e)
+        for t in layer.idx:
+            assert t.storage_offset() + t.shape[0] * t.stride(0) <= t.untyped_storage().nbytes() // 4
+        _check(_vq().gemv(layer, x, out_dtype=torch.float32), x, [data[e]], _offsets([3]), None, -3.0)
