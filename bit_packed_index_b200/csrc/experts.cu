@@ -182,6 +182,7 @@ struct Ctrl {
   uint64_t donea[kGroups];    // of step % kGroups: its products are done
   uint64_t fullx[kMaxX], emptyx[kMaxX];
   uint64_t accf[2], acce[2];
+  uint64_t idle;              // every product issued is done
   uint32_t tmem;
   int abort;
   int last;                                       // the epilogue's CTA is the last at a joined tile
@@ -533,6 +534,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&ctrl->accf[b], 1);
       mbar_init(&ctrl->acce[b], 4);
     }
+    mbar_init(&ctrl->idle, 1);
     ctrl->abort = 0;
     fence_barrier_init();
   }
@@ -645,9 +647,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     }
-    if (*abort_flag && lane == 0)                     // loads in flight land before the block ends
+    // Loads in flight land before the block ends, whichever warp gives up and
+    // when (the products wait for them anyway).
+    if (lane == 0)
       for (int i = max(0, issued - g.nx); i < issued; ++i)
         drain_phase(&ctrl->fullx[i % g.nx], (i / g.nx) & 1, kDrain / 16);
+    __syncwarp();
   } else if (warp == 1) {                             // products
     const uint64_t adesc0 = sw128_kmajor_desc(smem_addr(aring)), xdesc0 = sw128_kmajor_desc(smem_addr(xring));
     const uint32_t xstep = static_cast<uint32_t>(g.xslot) >> 4;
@@ -767,10 +772,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!stop && elect_one()) umma_commit(&ctrl->accf[buf]);
       __syncwarp();
     }
-    if (*abort_flag) {                                // products in flight end before tensor memory is freed
-      const long long t0 = clock64();
-      while (clock64() - t0 < kDrain / 16) __nanosleep(1000);
+    if (elect_one()) {                                // products in flight end before tensor memory is freed, as above
+      umma_commit(&ctrl->idle);
+      drain_phase(&ctrl->idle, 0, kDrain);
     }
+    __syncwarp();
   } else if (warp >= 4 && warp < 8) {                 // epilogue: lane quarter warp & 3, one W row per thread
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int lq = warp & 3, r = 32 * lq + lane;

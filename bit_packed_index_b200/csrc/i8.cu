@@ -324,7 +324,9 @@ __global__ void __launch_bounds__(kNarrowThreads) gemm_i8_narrow_kernel(const __
         sp ^= 1;
       }
     }
-    if (*abort_flag && lane == 0)                            // loads in flight land before the block ends
+    // Loads in flight land before the block ends, whichever warp gives up and
+    // when (the products wait for them anyway).
+    if (lane == 0)
       for (int i = max(0, issued - g.stages); i < issued; ++i)
         drain_phase(&ctrl->full[i % g.stages], (i / g.stages) & 1, kDrain);
   } else if (warp == 1) {
@@ -499,12 +501,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1)
     // the last products' arrivals on this CTA's barriers are in
     for (int i = max(0, gs - g.stages); i < gs && !stop; ++i)
       stop = !warp_wait(&ctrl->empty[i % g.stages], (i / g.stages) & 1, abort_flag, g.status, g.budget);
-    if (*abort_flag) {
-      // Loads in flight land before the block ends.  Their barriers may
-      // never complete once one CTA of the pair has given up, so time does.
-      const long long t0 = clock64();
-      while (clock64() - t0 < kDrain / 16) __nanosleep(1000);
-    }
   } else if (warp == 1) {
     if (rank == 0) {
       const uint32_t idesc = i8_idesc(2 * kRows, g.tn);
@@ -538,10 +534,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1)
         }
         if (!stop && elect_one()) umma_commit_pair(&ctrl->accf[buf]);
         __syncwarp();
-      }
-      if (*abort_flag) {                                     // products in flight end before tensor memory is freed
-        const long long t0 = clock64();
-        while (clock64() - t0 < kDrain / 16) __nanosleep(1000);
       }
     }
   } else if (warp >= 4) {
@@ -583,6 +575,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1)
   tc_fence_before();
   cluster_arrive();
   cluster_wait();
+  if (*abort_flag) {
+    // Loads and products in flight end before tensor memory is freed and the
+    // block ends.  Their barriers may never complete once a CTA of the pair has
+    // given up, so time does.  No warp raises the flag behind the barrier above;
+    // a CTA whose flag is down has seen all of its loads and products end.
+    const long long t0 = clock64();
+    while (clock64() - t0 < kDrain / 16) __nanosleep(1000);
+    __syncwarp();
+  }
   if (warp == 2) {
     tc_fence_after();
     tmem_dealloc_pair(tmem, kWideCols);

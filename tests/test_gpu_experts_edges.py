@@ -62,3 +62,27 @@ def test_one_of_those_experts_as_a_layer(n):
         for t in layer.idx:
             assert t.storage_offset() + t.shape[0] * t.stride(0) <= t.untyped_storage().nbytes() // 4
         _check(_vq().gemv(layer, x, out_dtype=torch.float32), x, [data[e]], _offsets([3]), None, -3.0)
+
+
+# ---- blocks that give up -------------------------------------------------------
+@pytest.mark.parametrize("budget", ["0", "1500", "6000"])
+@pytest.mark.parametrize("kin,counts", [(200, [3, 0, 2]), (1000, [300, 40, 700]), (1000, [1, 0, 0])])
+def test_calls_after_ones_that_gave_up(monkeypatch, kin, counts, budget):
+    """Waits run out early, in the middle or not at all; whatever a block had in
+    flight has landed before the next call's blocks take its place: that call,
+    launched right behind, is right every time."""
+    vq = _vq()
+    data, ex = _experts(LayerSpec(900, kin, 8, (12, 8), (0.02, 0.005)), 3, "tile4", 31)
+    x, offsets = torch.randn((sum(counts), kin), device="cuda").bfloat16(), _offsets(counts)
+    want = _run(ex, x, offsets)
+    _check(want, x, data, offsets, None, -3.0)
+    work = torch.zeros(vq.gemm_experts_workspace_size(ex, sum(counts)), dtype=torch.uint8, device="cuda")
+    spoilt, ys = torch.empty_like(want), []
+    for _ in range(20):
+        monkeypatch.setenv("VQ_WAIT_BUDGET", budget)
+        vq.gemm_experts(ex, x, offsets, out=spoilt, workspace=work)
+        monkeypatch.delenv("VQ_WAIT_BUDGET")
+        ys.append(vq.gemm_experts(ex, x, offsets, out_dtype=torch.float32))
+    torch.cuda.synchronize()
+    assert int(work[:4].view(torch.int32)) in (vq.VQ_OK, vq.VQ_ERR_TIMEOUT)
+    assert all(torch.equal(y, want) for y in ys)
