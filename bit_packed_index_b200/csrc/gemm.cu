@@ -301,12 +301,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (MODE == kStaged) tma_load_2d(a + MSUB * kATile, &tmap_b, &ctrl->full[s], kt * BK, n0);
         issued = kt + 1;
       }
-      if (*abort_flag) {   // let loads already in flight land before the block exits
-        // (with fused tiles a stage also waits for the producers, who may have
-        // given up: then the time bound, far above a load's latency, ends it)
-        for (int kt = max(0, issued - g.stages); kt < issued; ++kt)
-          drain_phase(&ctrl->full[kt % g.stages], (kt / g.stages) & 1, kWaitBudget / 64);
-      }
+      // Loads in flight land before the block exits, whichever warp gives up and
+      // when (with fused tiles a stage also waits for the producers, who may have
+      // given up: then the time bound, far above a load's latency, ends it).
+      for (int kt = max(0, issued - g.stages); kt < issued; ++kt)
+        drain_phase(&ctrl->full[kt % g.stages], (kt / g.stages) & 1, kWaitBudget / 64);
     }
   } else if (warp == 1) {
     if (lane == 0) {                                   // MMA issuer

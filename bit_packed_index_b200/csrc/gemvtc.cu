@@ -168,10 +168,9 @@ __global__ void __launch_bounds__(kTcThreads) gemv_tc_kernel(const __grid_consta
         tma_load_2d(stages + s * kTcStage + kTcATile, &xmap, &ctrl->xfull[s], (kt0 + i) * kTcK, 0);
         issued = i + 1;
       }
-      if (*abort_flag) {   // let loads already in flight land before the block exits
-        for (int i = max(0, issued - kTcStages); i < issued; ++i)
-          drain_phase(&ctrl->xfull[i % kTcStages], (i / kTcStages) & 1, 4000000000LL);
-      }
+      // loads in flight land before the block exits, whichever warp gives up and when
+      for (int i = max(0, issued - kTcStages); i < issued; ++i)
+        drain_phase(&ctrl->xfull[i % kTcStages], (i / kTcStages) & 1, 4000000000LL);
     }
   } else if (warp == 1) {
     if (lane == 0) {                                   // MMA issuer
@@ -461,10 +460,9 @@ __global__ void __launch_bounds__(TsShape<LAYOUT>::threads, 1) gemv_tcs_kernel(c
                           &ctrl->xf[q]);
         }
       }
-      if (*abort_flag) {   // let loads already in flight land before the block exits
-        for (int i = max(0, gs - xs); i < gs; ++i)
-          drain_phase(&ctrl->xf[i % xs], (i / xs) & 1, 4000000000LL);
-      }
+      // loads in flight land before the block exits, whichever warp gives up and when
+      for (int i = max(0, gs - xs); i < gs; ++i)
+        drain_phase(&ctrl->xf[i % xs], (i / xs) & 1, 4000000000LL);
     }
   } else if (warp == 1) {
     if (lane == 0) {                                   // MMA issuer
