@@ -34,12 +34,16 @@ __device__ __forceinline__ Layer expert_layer(const Experts& E, int x) {
 }
 
 // ---------------------------------------------------------------------------
-// x' = x * 2^-e in fp16, one row per grouped row, with 2^e and sum_k x.  e puts
-// the row's largest magnitude in [2^14, 2^15).  Vector j of the layer (d
-// values) takes columns H j .. H j + d - 1, H = 8 (d <= 8) or 16, zeros in the
-// rest, so that the weight tiles hold centroids in whole 16-byte chunks.
+// x' = x * 2^-e in fp16, one row per grouped row, with 2^e and kSumUnit sum_k x.
+// e puts the row's largest magnitude in [2^15, 2^16) (bf16 and fp16 values there
+// are exact in fp16), so 2^e is at most 2^112 and times any fp16 scale stays in
+// fp32's range; so does the sum of 2^24 of the largest values in its unit.
+// Vector j of the layer (d values) takes columns H j .. H j + d - 1, H = 8 (d <=
+// 8) or 16, zeros in the rest, so that the weight tiles hold centroids in whole
+// 16-byte chunks.
 // ---------------------------------------------------------------------------
 constexpr int kPrepThreads = 256;
+constexpr float kSumUnit = 1.0f / (1 << 24);
 
 __device__ __forceinline__ float value16(uint16_t u, int x_fp16) { return x_fp16 ? h2f(u) : bf2f(u); }
 
@@ -69,14 +73,14 @@ __global__ void __launch_bounds__(kPrepThreads) experts_prep_kernel(
         const float lo = value16(static_cast<uint16_t>(w[i] & 0xFFFFu), x_fp16);
         const float hi = value16(static_cast<uint16_t>(w[i] >> 16), x_fp16);
         mx = fmaxf(mx, fmaxf(fabsf(lo), fabsf(hi)));
-        sm += lo;
-        sm += hi;
+        sm = fmaf(lo, kSumUnit, sm);
+        sm = fmaf(hi, kSumUnit, sm);
       }
     }
     for (int k = 8 * whole + tid; k < kin; k += kPrepThreads) {
       const float v = value16(__ldg(xr + k), x_fp16);
       mx = fmaxf(mx, fabsf(v));
-      sm += v;
+      sm = fmaf(v, kSumUnit, sm);
     }
   }
 #pragma unroll
@@ -96,7 +100,7 @@ __global__ void __launch_bounds__(kPrepThreads) experts_prep_kernel(
     sm += s_sum[w];
   }
   int e = 0;
-  if (mx > 0.0f && mx < INFINITY) e = max(-126, min(127, static_cast<int>(__float_as_uint(mx) >> 23) - 126 - 15));
+  if (mx > 0.0f && mx < INFINITY) e = max(-126, min(127, static_cast<int>(__float_as_uint(mx) >> 23) - 127 - 15));
   const float f1 = __uint_as_float(static_cast<uint32_t>(127 - e / 2) << 23);   // 2^-e as two normal factors
   const float f2 = __uint_as_float(static_cast<uint32_t>(127 - (e - e / 2)) << 23);
   const int chunks = static_cast<int>(kp / 8), per = d > 8 ? 2 : 1;
@@ -432,10 +436,11 @@ struct Maps {
 };
 
 // y of one output (its column in y: yo) for `n` of sixteen rows from their
-// sums: s v 2^e + t sum x + b.  scales: 2^e and sum x of the rows, in shared
-// memory.  The type is a template argument: a branch on it per value, with the
-// single warp that each scheduler has for this, made the store of a tile take
-// longer than its products.
+// sums: s v 2^e + t sum x + b, t in units of 1 / kSumUnit.  scales: 2^e and
+// kSumUnit sum x of the rows, in shared memory.  s 2^e comes first: v 2^e can
+// leave fp32's range where y does not.  The type is a template argument: a
+// branch on it per value, with the single warp that each scheduler has for
+// this, made the store of a tile take longer than its products.
 template <int YT>
 __device__ __forceinline__ void store_rows(uint8_t* yo, int64_t ldb, const float (&v)[16], int n, const float4* scales,
                                            float sc, float tb, float ob) {
@@ -443,7 +448,7 @@ __device__ __forceinline__ void store_rows(uint8_t* yo, int64_t ldb, const float
 #pragma unroll
   for (int i = 0; i < 16; i += 2) {
     const float4 e = scales[i / 2];
-    const float a = sc * (v[i] * e.x) + (tb * e.y + ob), b = sc * (v[i + 1] * e.z) + (tb * e.w + ob);
+    const float a = fmaf(sc * e.x, v[i], fmaf(tb, e.y, ob)), b = fmaf(sc * e.z, v[i + 1], fmaf(tb, e.w, ob));
     T x, y;
     if constexpr (YT == VQ_FP32) {
       x = a;
@@ -791,7 +796,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const Layer L = expert_layer(g.E, t.expert);
       const bool live = o < L.n;
       const float sc = live && L.scale ? h2f(__ldg(L.scale + o)) : 1.0f;
-      const float tb = live && L.bias ? h2f(__ldg(L.bias + o)) : 0.0f;
+      const float tb = live && L.bias ? h2f(__ldg(L.bias + o)) * (1.0f / kSumUnit) : 0.0f;
       const float ob = live ? out_bias_of(L.ob, o) : 0.0f;
       // the rows' scales and sums, in the table that the tile before last used
       float2* scales = s_scales + (it & 1) * g.tokens;

@@ -86,3 +86,42 @@ def test_calls_after_ones_that_gave_up(monkeypatch, kin, counts, budget):
     torch.cuda.synchronize()
     assert int(work[:4].view(torch.int32)) in (vq.VQ_OK, vq.VQ_ERR_TIMEOUT)
     assert all(torch.equal(y, want) for y in ys)
+
+
+# ---- rows near the end of bf16's range ------------------------------------------
+@pytest.mark.parametrize("od", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("bias", [None, 1e-3])
+@pytest.mark.parametrize("books,layout", [((12, 8), "tile4"), ((16,), "rows"), ((9, 4), "rows")])
+def test_finite_rows_have_finite_products(books, layout, bias, od):
+    """Rows whose sums pass fp32's range while y does not; the rows beside them
+    keep every bit."""
+    spec = LayerSpec(300, 4096, 8, books, (0.02, 0.005)[: len(books)], (0.5, 1.5), bias, out_bias_std=1.0)
+    data, ex = _experts(spec, 2, layout, 12)
+    x = torch.randn((40, 4096), device="cuda").bfloat16()
+    offsets = _offsets([17, 20])
+    plain = _run(ex, x, offsets, od=od)
+    big = [1, 2, 5, 16, 20, 36]
+    x[1] = 1e35                                     # 4096 of them: sum x = 4.1e38
+    x[2] = -1e35
+    x[5] = torch.where(torch.arange(4096, device="cuda") % 2 == 0, 3e38, -3e38).bfloat16() * 2.0 ** -6
+    x[16] = 2.0 ** 64                               # the first that counts as big
+    x[20, :7], x[20, 7:] = 3e38, 0
+    x[36] = 1e36 * torch.randn(4096, device="cuda")
+    y = _run(ex, x, offsets, od=od)
+    _check(y, x, data, offsets, None, -3.0)
+    keep = [i for i in range(40) if i not in big]
+    assert torch.equal(y[keep], plain[keep])
+
+
+@pytest.mark.parametrize("value", [3.3e38, 1e-30])
+def test_the_largest_scales(value):
+    """Scales up to fp16's largest on rows of one value, centroids so small that
+    y stays in range."""
+    spec = LayerSpec(150, 64, 8, (8,), (1e-6,), (30000.0, 65000.0), None)
+    data, ex = _experts(spec, 1, "rows", 4)
+    x = torch.zeros((3, 64), device="cuda")
+    x[0, 5], x[2, 63] = value, -value
+    x = x.bfloat16()
+    y = _run(ex, x, _offsets([3]))
+    _check(y, x, data, _offsets([3]), None, -3.0)
+    assert y.isfinite().all()
