@@ -164,7 +164,7 @@ __global__ void __launch_bounds__(kGvThreads) gemv_kernel(
           if (lane == 0 && orow < o_end && b < batch) {
             const float sc = L.scale ? h2f(L.scale[orow]) : 1.0f;
             const float t = L.bias ? h2f(L.bias[orow]) : 0.0f;
-            float val = sc * dot + t * xsum[b];
+            float val = sc * dot + t * bias_sum(t, xsum[b]);
             if (split == 0) val += out_bias_of(L.ob, orow);   // once, with split 0's part
             if (ws) ws[(static_cast<int64_t>(split) * batch + b) * L.n + orow] = val;
             else store_out(y, yt, b * ldy + orow, val);

@@ -1019,7 +1019,7 @@ __global__ void __launch_bounds__(256, 8) gemv_lut_finalize(const float* __restr
     const int o = v - out.row0[l];
     const float sc = out.scale[l] ? h2f(out.scale[l][o]) : 1.0f;
     const float tb = out.bias[l] ? h2f(out.bias[l][o]) : 0.0f;
-    store_out(out.y[l], yt, o, sc * t + tb * s_xsum + out_bias_of(out.ob[l], o));
+    store_out(out.y[l], yt, o, sc * t + tb * bias_sum(tb, s_xsum) + out_bias_of(out.ob[l], o));
   }
 }
 

@@ -198,6 +198,10 @@ __device__ __forceinline__ uint32_t load_field(const uint32_t* __restrict__ row,
 __device__ __forceinline__ float h2f(uint16_t h) { return __half2float(__ushort_as_half(h)); }
 // Output bias of row o (0 without one).
 __device__ __forceinline__ float out_bias_of(const uint16_t* ob, int o) { return ob ? h2f(ob[o]) : 0.0f; }
+// What the sum over k of x may count for under a bias of t: nothing under a
+// bias of zero (a layer without one), also where the sum of finite values has
+// left fp32's range and the product with zero would be NaN.
+__device__ __forceinline__ float bias_sum(float t, float sum) { return t != 0.0f ? sum : 0.0f; }
 __device__ __forceinline__ float bf2f(uint16_t h) {
   return __bfloat162float(__ushort_as_bfloat16(h));
 }
