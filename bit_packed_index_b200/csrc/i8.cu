@@ -390,7 +390,10 @@ __global__ void __launch_bounds__(kNarrowThreads) gemm_i8_narrow_kernel(const __
   if (splits > 1) {
     cluster_arrive();
     cluster_wait();
-    // this CTA's share of the tile's outputs
+    // This CTA's share of the tile's outputs.  The activation scales come from
+    // its table: the kernel may have started before the one that wrote them
+    // ended, so they are not constant over its life and no load of constant
+    // data (__ldg) may fetch them.
     const int total = g.m * kRows, share = (total + splits - 1) / splits;
     const int last = min(total, (split + 1) * share);
     if (!*abort_flag) {
@@ -403,7 +406,7 @@ __global__ void __launch_bounds__(kNarrowThreads) gemm_i8_narrow_kernel(const __
           sum += v;
         }
         const int c = i / kRows, o = row0 + (i & (kRows - 1));
-        if (o < g.n) store_out(g.y, g.yt, c * g.ldy + o, i8_out(sum, g.ws[o], __ldg(g.qs + c), out_bias_of(g.ob, o)));
+        if (o < g.n) store_out(g.y, g.yt, c * g.ldy + o, i8_out(sum, g.ws[o], ctrl->scales[c], out_bias_of(g.ob, o)));
       }
     }
     cluster_arrive();                                        // no CTA leaves while others read its sums

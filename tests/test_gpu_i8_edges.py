@@ -30,3 +30,21 @@ def test_calls_after_ones_that_gave_up(monkeypatch, m, n, k, budget):
     torch.cuda.synchronize()
     assert int(work[:4].view(torch.int32)) in (vq.VQ_OK, vq.VQ_ERR_TIMEOUT)
     assert all(torch.equal(y, want) for y in ys)
+
+
+@pytest.mark.parametrize("m,n,k", [(1, 1024, 16384), (3, 1000, 4200), (40, 700, 2049)])
+def test_rows_in_turn_through_a_product_split_along_k(m, n, k):
+    """linear_i8's product starts under the quantisation of its own rows: with
+    rows of very different sizes in turn, each call takes its own scales."""
+    vq = _vq()
+    w, ws, b = _weights(n, k, 6, False)
+    layer = vq.Int8Layer(w, ws, b)
+    xs = [(torch.randn((m, k), device="cuda") * s).bfloat16() for s in (1.0, 1e-6, 1e6)]
+    want = []
+    for x in xs:
+        q, s = vq.quant_i8(x)
+        want.append(vq.gemm_i8(layer, q, s, out_dtype=torch.float32))
+    work = torch.zeros(vq.linear_i8_workspace_size(layer, m), dtype=torch.uint8, device="cuda")
+    got = [vq.linear_i8(layer, xs[i % 3], out_dtype=torch.float32, workspace=work) for i in range(60)]
+    torch.cuda.synchronize()
+    assert all(torch.equal(got[i], want[i % 3]) for i in range(60))
