@@ -195,7 +195,7 @@ struct I8Args {
   int64_t ldy;
   int* status;
   long long budget;
-  int kt_per_split;       // narrow kernel: steps of a CTA of the cluster
+  int split_log2;         // narrow kernel: log2 of the CTAs of a cluster
   int tiles_n, tiles_m;   // wide kernel: tiles of 256 outputs, of tn rows
   int stages;
 };
@@ -274,8 +274,8 @@ __global__ void __launch_bounds__(kNarrowThreads) gemm_i8_narrow_kernel(const __
   const int warp = uniform(static_cast<int>(threadIdx.x >> 5)), lane = threadIdx.x & 31;
   const int splits = gridDim.y, split = blockIdx.y;          // the cluster spans the grid's y
   const int row0 = blockIdx.x * kRows;
-  const int kt0 = split * g.kt_per_split;
-  const int nkt = max(0, min(g.num_kt, kt0 + g.kt_per_split) - kt0);
+  const int kt0 = split * g.num_kt >> g.split_log2;          // even runs: they differ by a step at most
+  const int nkt = ((split + 1) * g.num_kt >> g.split_log2) - kt0;
   int issued = 0;                                            // warp 0: steps loaded
   volatile int* abort_flag = &ctrl->abort;
 
@@ -377,7 +377,7 @@ __global__ void __launch_bounds__(kNarrowThreads) gemm_i8_narrow_kernel(const __
         tmem_ld16(t + c, acc);
         tmem_wait_ld();
 #pragma unroll
-        for (int i = 0; i < 16; ++i) red[(c + i) * kRows + r] = nkt ? static_cast<int>(acc[i]) : 0;
+        for (int i = 0; i < 16; ++i) red[(c + i) * kRows + r] = static_cast<int>(acc[i]);
       }
     }
   }
@@ -643,11 +643,12 @@ long long wait_budget() {
   return 4000000000LL;
 }
 
-// Splits of the narrow kernel: double the cluster while the grid stays within
-// two CTAs per SM and each CTA keeps at least four steps (512 bytes of k).
-// 24 x 8192 x 8192 with 2, 4 (chosen) and 8 CTAs a cluster: 18.0, 16.4, 19.8 us;
-// 4 x 4096 x 4096 with 4 and 8 (chosen): 5.3, 5.8; 16 x 14336 x 4096 with 1 and 2
-// (chosen): 14.1, 15.6.
+// Splits of the narrow kernel (a power of two): double the cluster while the
+// grid stays within two CTAs per SM and each CTA keeps at least four steps (512
+// bytes of k).  24 x 8192 x 8192 with 2, 4 (chosen) and 8 CTAs a cluster: 18.0,
+// 16.4, 19.8 us.  It doubles once too often
+// where the cluster's barriers cost more than the loads gain: 4 x 4096 x 4096 with
+// 4 and 8 (chosen) 5.3, 5.8; 16 x 14336 x 4096 with 1 and 2 (chosen) 14.1, 15.6.
 int narrow_splits(int tiles, int num_kt, int sms) {
   int s = 1;
   while (s < 8 && tiles * s * 2 <= 2 * sms && num_kt >= 8 * s) s *= 2;
@@ -723,7 +724,7 @@ vq_status launch_gemm_i8(const I8Layer& L, const int8_t* q, int64_t ldq, const f
   if (narrow) {
     const int tiles = (L.n + kRows - 1) / kRows;
     const int splits = narrow_splits(tiles, g.num_kt, sms);
-    g.kt_per_split = (g.num_kt + splits - 1) / splits;
+    for (g.split_log2 = 0; 1 << g.split_log2 < splits; ++g.split_log2) {}
     g.stages = std::min(kMaxStages, (device_smem_optin() / 2 - 1024 - kCtrlBytes - 1024) / stage);   // two CTAs per SM
     cfg.gridDim = dim3(tiles, splits);
     cfg.blockDim = dim3(kNarrowThreads);

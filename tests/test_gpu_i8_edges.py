@@ -48,3 +48,16 @@ def test_rows_in_turn_through_a_product_split_along_k(m, n, k):
     got = [vq.linear_i8(layer, xs[i % 3], out_dtype=torch.float32, workspace=work) for i in range(60)]
     torch.cuda.synchronize()
     assert all(torch.equal(got[i], want[i % 3]) for i in range(60))
+
+
+@pytest.mark.parametrize("steps", [8, 9, 15, 16, 17, 31, 32, 33, 49, 57, 64])
+@pytest.mark.parametrize("m", [1, 33])
+def test_runs_of_k_of_every_length(m, steps):
+    """Steps of 128 values that two, four and eight CTAs share, evenly or not."""
+    vq = _vq()
+    k = 128 * steps - 5
+    w, ws, b = _weights(300, k, steps, True)
+    q = torch.empty((m, 128 * steps), dtype=torch.int8, device="cuda").fill_(-55)[:, :k]
+    q.copy_(torch.randint(-128, 128, (m, k), device="cuda", dtype=torch.int8))
+    s = torch.rand(m, device="cuda")
+    _check(vq.gemm_i8(vq.Int8Layer(w, ws, b), q, s, out_dtype=torch.float32), q, s, w, ws, b)
