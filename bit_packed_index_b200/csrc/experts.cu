@@ -77,7 +77,7 @@ __global__ void __launch_bounds__(kPrepThreads) experts_prep_kernel(
         sm = fmaf(hi, kSumUnit, sm);
       }
     }
-    for (int k = 8 * whole + tid; k < kin; k += kPrepThreads) {
+    for (uint32_t k = 8 * whole + tid; k < static_cast<uint32_t>(kin); k += kPrepThreads) {
       const float v = value16(__ldg(xr + k), x_fp16);
       mx = fmaxf(mx, fabsf(v));
       sm = fmaf(v, kSumUnit, sm);
@@ -103,10 +103,11 @@ __global__ void __launch_bounds__(kPrepThreads) experts_prep_kernel(
   if (mx > 0.0f && mx < INFINITY) e = max(-126, min(127, static_cast<int>(__float_as_uint(mx) >> 23) - 127 - 15));
   const float f1 = __uint_as_float(static_cast<uint32_t>(127 - e / 2) << 23);   // 2^-e as two normal factors
   const float f2 = __uint_as_float(static_cast<uint32_t>(127 - (e - e / 2)) << 23);
-  const int chunks = static_cast<int>(kp / 8), per = d > 8 ? 2 : 1;
-  for (int g = tid; g < chunks; g += kPrepThreads) {
-    const int first = (g / per) * d + 8 * (g % per);       // element in column 8 g
-    const int n = live ? min(min(8, d - 8 * (g % per)), kin - first) : 0;
+  const uint32_t chunks = static_cast<uint32_t>(kp / 8), per = d > 8 ? 2 : 1;   // up to 2^31
+  for (uint32_t g = tid; g < chunks; g += kPrepThreads) {
+    const int at = 8 * static_cast<int>(g % per);
+    const int64_t first = static_cast<int64_t>(g / per) * d + at;      // element in column 8 g
+    const int n = live ? static_cast<int>(min(static_cast<int64_t>(min(8, d - at)), kin - first)) : 0;
     float v[8];
     if (vec && d % 8 == 0 && n == 8) {
       const uint4 q = __ldg(reinterpret_cast<const uint4*>(xr + first));
@@ -352,7 +353,7 @@ struct Words {
       stride = L.rw[m];
       base = L.idx[m] + ((o * (4 * B)) >> 5);
       shift = static_cast<int>((o * (4 * B)) & 31);
-      tiles = (L.nvec + 3) / 4;
+      tiles = (L.nvec - 1) / 4 + 1;
     } else {
       stride = (static_cast<int64_t>(L.nvec) * B + 127) / 128 * 4;
       base = L.idx[m] + o * L.rw[m];
@@ -1185,9 +1186,9 @@ Plan plan_experts(const Experts& E, int m) {
   Plan p{};
   const Layer& L = E.L;
   const int per = L.d > 8 ? 4 : 8;                             // vectors of a step
-  p.nkt = (L.nvec + per - 1) / per;
+  p.nkt = (L.nvec - 1) / per + 1;
   p.kp = static_cast<int64_t>(p.nkt) * 64;
-  p.row_tiles = (L.n + kRowTile - 1) / kRowTile;
+  p.row_tiles = (L.n - 1) / kRowTile + 1;
   p.ctas = device_sm_count();
   // What comes first: books in shared memory (both, the first, the second; one
   // of more than 2^13 entries never fits), then the token tile (W is decoded once

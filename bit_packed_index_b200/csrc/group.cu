@@ -231,7 +231,7 @@ __global__ void __launch_bounds__(kCombineThreads, kCombineBlocks) combine_rows_
     const T* __restrict__ z, int z_rows, int n, int64_t ldz, const int32_t* __restrict__ pos,
     const float* __restrict__ weight, int64_t ld_weight, int n_tokens, int top_k, void* __restrict__ y, vq_dtype yt,
     int64_t ldy) {
-  const int groups = (n + 7) / 8;
+  const int groups = n / 8 + (n % 8 != 0);
   const int64_t total = static_cast<int64_t>(n_tokens) * groups;
   for (int64_t i = blockIdx.x * static_cast<int64_t>(kCombineThreads) + threadIdx.x; i < total;
        i += static_cast<int64_t>(gridDim.x) * kCombineThreads) {
@@ -242,7 +242,7 @@ __global__ void __launch_bounds__(kCombineThreads, kCombineBlocks) combine_rows_
     float acc[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) acc[e] = 0.0f;
-    if (VEC && c + 8 <= n) {
+    if (VEC && n - c >= 8) {
       for (int j0 = 0; j0 < top_k; j0 += kCombineAhead) {
         Load8<T> q[kCombineAhead];
         float w[kCombineAhead];
@@ -297,7 +297,7 @@ cudaError_t launch_combine(bool vec, const void* z, int z_rows, int n, int64_t l
                            const float* weight, int64_t ld_weight, int n_tokens, int top_k, void* y, vq_dtype yt,
                            int64_t ldy, cudaStream_t stream) {
   auto k = vec ? combine_rows_kernel<T, true> : combine_rows_kernel<T, false>;
-  const int64_t total = static_cast<int64_t>(n_tokens) * ((n + 7) / 8);
+  const int64_t total = static_cast<int64_t>(n_tokens) * ((static_cast<int64_t>(n) + 7) / 8);
   const int64_t most = static_cast<int64_t>(device_sm_count()) *
                        resident_blocks_per_sm(reinterpret_cast<const void*>(k), kCombineThreads, 0) * 8;
   const int grid = static_cast<int>(std::min<int64_t>((total + kCombineThreads - 1) / kCombineThreads, most));

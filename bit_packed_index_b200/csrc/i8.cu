@@ -76,7 +76,7 @@ __global__ void __launch_bounds__(1024) quant_i8_kernel(const uint16_t* __restri
   uint32_t top = 0;                                   // two 16-bit maxima of |x|
   uint4 u[V > 0 ? V : 1];
   if constexpr (V > 0) {
-    const int groups = (n + 7) / 8;
+    const int groups = n / 8 + (n % 8 != 0);
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       const int g = v * blockDim.x + tid;
@@ -99,7 +99,9 @@ __global__ void __launch_bounds__(1024) quant_i8_kernel(const uint16_t* __restri
       top = __vmaxu2(top, __vmaxu2(u[v].z & 0x7FFF7FFFu, u[v].w & 0x7FFF7FFFu));
     }
   } else {
-    for (int k = tid; k < n; k += blockDim.x) top = max(top, static_cast<uint32_t>(__ldg(xr + k)) & 0x7FFFu);
+    // (unsigned: k passes 2^31 behind the longest rows)
+    for (uint32_t k = tid; k < static_cast<uint32_t>(n); k += blockDim.x)
+      top = max(top, static_cast<uint32_t>(__ldg(xr + k)) & 0x7FFFu);
   }
   top = max(top & 0xFFFFu, top >> 16);
   top = __reduce_max_sync(0xffffffffu, top);
@@ -113,7 +115,7 @@ __global__ void __launch_bounds__(1024) quant_i8_kernel(const uint16_t* __restri
   if (bad) s = 0.0f;                                  // q = 0
   const float inv = s >= kTinyScale ? __fdiv_rn(1.0f, s) : 0.0f;
   if constexpr (V > 0) {
-    const int groups = (n + 7) / 8;
+    const int groups = n / 8 + (n % 8 != 0);
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       const int g = v * blockDim.x + tid;
@@ -134,7 +136,7 @@ __global__ void __launch_bounds__(1024) quant_i8_kernel(const uint16_t* __restri
       }
     }
   } else {
-    for (int k = tid; k < n; k += blockDim.x)
+    for (uint32_t k = tid; k < static_cast<uint32_t>(n); k += blockDim.x)
       qr[k] = static_cast<int8_t>(quant_one(val16<FP16>(__ldg(xr + k)), s, inv));
   }
 }
@@ -143,7 +145,7 @@ template <bool FP16>
 cudaError_t launch_quant(const uint16_t* x, int rows, int n, int64_t ldx, int8_t* q, int64_t ldq, float* scale,
                          cudaStream_t stream) {
   const bool vec = aligned(x, 16) && ldx % 8 == 0 && aligned(q, 8) && ldq % 8 == 0;
-  const int groups = (n + 7) / 8;
+  const int groups = n / 8 + (n % 8 != 0);
   // threads: about two groups each, so that a row's loads are all in flight
   // and short rows leave room for many blocks
   int threads = 64;
@@ -646,9 +648,9 @@ long long wait_budget() {
 // Splits of the narrow kernel (a power of two): double the cluster while the
 // grid stays within two CTAs per SM and each CTA keeps at least four steps (512
 // bytes of k).  24 x 8192 x 8192 with 2, 4 (chosen) and 8 CTAs a cluster: 18.0,
-// 16.4, 19.8 us.  It doubles once too often
-// where the cluster's barriers cost more than the loads gain: 4 x 4096 x 4096 with
-// 4 and 8 (chosen) 5.3, 5.8; 16 x 14336 x 4096 with 1 and 2 (chosen) 14.1, 15.6.
+// 16.4, 19.8 us.  It doubles once too often where the cluster's barriers cost
+// more than the loads gain: 4 x 4096 x 4096 with 4 and 8 (chosen) 5.3, 5.8; 16 x
+// 14336 x 4096 with 1 and 2 (chosen) 14.1, 15.6.
 int narrow_splits(int tiles, int num_kt, int sms) {
   int s = 1;
   while (s < 8 && tiles * s * 2 <= 2 * sms && num_kt >= 8 * s) s *= 2;
@@ -704,7 +706,7 @@ vq_status launch_gemm_i8(const I8Layer& L, const int8_t* q, int64_t ldq, const f
     g.tn = (m + 15) / 16 * 16;
     box = g.tn;
   } else {
-    g.tiles_n = (L.n + 2 * kRows - 1) / (2 * kRows);
+    g.tiles_n = (L.n - 1) / (2 * kRows) + 1;
     g.tn = wide_rows(m, g.tiles_n, sms / 2);
     g.tiles_m = (m + g.tn - 1) / g.tn;
     box = g.tn / 2;
@@ -722,7 +724,7 @@ vq_status launch_gemm_i8(const I8Layer& L, const int8_t* q, int64_t ldq, const f
   attr[0].val.programmaticStreamSerializationAllowed = pdl ? 1 : 0;
   const void* k;
   if (narrow) {
-    const int tiles = (L.n + kRows - 1) / kRows;
+    const int tiles = (L.n - 1) / kRows + 1;
     const int splits = narrow_splits(tiles, g.num_kt, sms);
     for (g.split_log2 = 0; 1 << g.split_log2 < splits; ++g.split_log2) {}
     g.stages = std::min(kMaxStages, (device_smem_optin() / 2 - 1024 - kCtrlBytes - 1024) / stage);   // two CTAs per SM

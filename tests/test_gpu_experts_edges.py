@@ -125,3 +125,17 @@ def test_the_largest_scales(value):
     y = _run(ex, x, _offsets([3]))
     _check(y, x, data, _offsets([3]), None, -3.0)
     assert y.isfinite().all()
+
+
+# ---- the longest rows -----------------------------------------------------------
+@pytest.mark.parametrize("n", [2 ** 31 - 1, 2 ** 31 - 8])
+def test_combining_the_longest_rows(n):
+    """One token of 2^31 - 1 columns (value by value) and of 2^31 - 8 (by words)."""
+    vq = _vq()
+    z = torch.zeros((1, n), dtype=torch.bfloat16, device="cuda")
+    at = [0, 9, 2 ** 30, n - 1025, n - 8, n - 1]
+    z[0, at] = torch.arange(1, 7, device="cuda").bfloat16()
+    y = vq.combine_rows(z, torch.zeros((1, 1), dtype=torch.int32, device="cuda"), torch.full((1, 1), 0.5, device="cuda"))
+    assert y[0, at].tolist() == [0.5, 1, 1.5, 2, 2.5, 3]
+    y[0, at] = 0
+    assert not any(bool(p.any()) for p in y[0].split(1 << 28))

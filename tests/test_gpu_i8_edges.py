@@ -61,3 +61,20 @@ def test_runs_of_k_of_every_length(m, steps):
     q.copy_(torch.randint(-128, 128, (m, k), device="cuda", dtype=torch.int8))
     s = torch.rand(m, device="cuda")
     _check(vq.gemm_i8(vq.Int8Layer(w, ws, b), q, s, out_dtype=torch.float32), q, s, w, ws, b)
+
+
+def test_quant_of_the_longest_row():
+    """2^31 - 1 values: positions pass 31 bits.  The row's largest is 127 times a
+    power of two, so the quotients of the sixteen other values are exact."""
+    vq = _vq()
+    n = 2 ** 31 - 1
+    x = torch.zeros((1, n), dtype=torch.bfloat16, device="cuda")
+    at = torch.tensor([0, 1, 7, 1023, 65536, 2 ** 20 + 3, 2 ** 30 - 1, 2 ** 30, 2 ** 31 - 1100, 2 ** 31 - 1024, 2 ** 31 - 1023,
+                       2 ** 31 - 1000, 2 ** 31 - 9, 2 ** 31 - 8, 2 ** 31 - 3], device="cuda")
+    x[0, at] = torch.arange(1, 16, device="cuda").bfloat16() / 4
+    x[0, -1] = -127 / 4
+    q, s = vq.quant_i8(x)
+    assert float(s) == 0.25 and q.shape == (1, n)
+    assert q[0, at].tolist() == list(range(1, 16)) and int(q[0, -1]) == -127
+    q[0, at], q[0, -1] = 0, 0
+    assert not any(bool(p.any()) for p in q[0].split(1 << 28))
