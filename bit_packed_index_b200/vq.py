@@ -588,6 +588,13 @@ def _scratch(nbytes: int, like: torch.Tensor, index: int, given: Optional[torch.
     return t.data_ptr(), nbytes, t
 
 
+def _accepted(size_fn: str, ref: int, rules: str):
+    """Refuse a description that no call would accept (host-only: the size of a call without rows)."""
+    status = getattr(lib(), size_fn)(ref, 0, C.byref(C.c_size_t(0)))
+    if status != VQ_OK:
+        raise ValueError(f"{rules} ({status_string(status)})")
+
+
 _functions = {}
 
 
@@ -628,6 +635,7 @@ class Int8Layer:
         self._desc = d
         self._ref = C.addressof(d)
         self._sizes = {}
+        _accepted("vq_gemm_i8_workspace_size", self._ref, "weight rows must start on 16 bytes and hold at most 131071 values")
 
     @classmethod
     def quantise(cls, w: torch.Tensor, out_bias: Optional[torch.Tensor] = None) -> "Int8Layer":
@@ -730,6 +738,7 @@ class Experts:
         _need(idx[0].dim() == 3 and idx[0].is_cuda, "idx must be stacked streams on a CUDA device")
         _need(1 <= vec_dim <= 16 and all(1 <= int(b) <= 16 for b in log2k), "vec_dim and log2k must lie in 1..16")
         dev, e = idx[0].device, idx[0].shape[0]
+        _need(e >= 1, "at least one expert")
         nvec = -(-in_features // vec_dim)
         stream_rows = out_features if layout == "rows" else -(-nvec // 4)
         D = _ExpertsDesc()
@@ -760,6 +769,8 @@ class Experts:
             setattr(d, name, t.data_ptr())
             setattr(D, name + "_stride", t.stride(0) if t.shape[0] > 1 else 0)
         D.n_experts = e
+        _accepted("vq_gemm_experts_workspace_size", C.addressof(D), "every expert's streams and books must start on 16 "
+                  "bytes, index rows be a multiple of 4 words apart, and experts number at most 1024")
         self.n_experts, self.out_features, self.in_features, self.vec_dim = e, out_features, in_features, vec_dim
         self.log2k, self.layout, self.device, self.index = [int(b) for b in log2k], layout, dev, idx[0].get_device()
         self.idx, self.codebooks = list(idx), list(codebooks)
@@ -771,6 +782,7 @@ class Experts:
     @classmethod
     def from_layers(cls, layers: Sequence[Layer]) -> "Experts":
         """Stack layers of one shape, layout and device (their tensors are copied)."""
+        _need(len(layers) >= 1, "at least one layer")
         a = layers[0]
         shape = lambda l: (l.out_features, l.in_features, l.vec_dim, list(l.log2k), l.layout, l.device,
                            [tuple(t.shape) for t in l.idx], l.scale is None, l.bias is None, l.out_bias is None)

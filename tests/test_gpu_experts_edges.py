@@ -139,3 +139,22 @@ def test_combining_the_longest_rows(n):
     assert y[0, at].tolist() == [0.5, 1, 1.5, 2, 2.5, 3]
     y[0, at] = 0
     assert not any(bool(p.any()) for p in y[0].split(1 << 28))
+
+
+# ---- descriptions that no call accepts ------------------------------------------
+def test_experts_that_no_call_accepts():
+    vq = _vq()
+    words = lambda *s: torch.zeros(s, dtype=torch.int32, device="cuda")
+    book = torch.zeros((2, 16, 8), dtype=torch.float16, device="cuda")
+    make = lambda idx, books=book, n=6, k=64: vq.Experts(n, k, 8, [4], [idx], [books])
+    make(words(2, 6, 12)[:, :, 4:8])
+    flat = torch.zeros(2 * 16 * 8 + 8, dtype=torch.float16, device="cuda")
+    for bad in (lambda: make(words(2, 6, 6)[:, :, :4]),                     # rows 6 words apart
+                lambda: make(words(2, 6, 8)[:, :, 2:6]),                    # starts on 8 bytes
+                lambda: make(words(2, 6, 4), flat[1:257].view(2, 16, 8)),   # a book that starts on 2
+                lambda: make(words(2, 6, 4), flat.as_strided((2, 16, 8), (132, 8, 1))),
+                lambda: make(words(1025, 6, 4), book[:1]),
+                lambda: make(words(0, 6, 4), book[:0]),
+                lambda: vq.Experts.from_layers([])):
+        with pytest.raises(ValueError):
+            bad()

@@ -78,3 +78,16 @@ def test_quant_of_the_longest_row():
     assert q[0, at].tolist() == list(range(1, 16)) and int(q[0, -1]) == -127
     q[0, at], q[0, -1] = 0, 0
     assert not any(bool(p.any()) for p in q[0].split(1 << 28))
+
+
+def test_layers_that_no_call_accepts():
+    """Refused when the layer is made: rows that do not start on 16 bytes, rows too long."""
+    vq = _vq()
+    base, ws = torch.zeros((4, 64), dtype=torch.int8, device="cuda"), torch.ones(4, device="cuda")
+    vq.Int8Layer(base[:, 16:48], ws)
+    for w in (base[:, 8:48], torch.zeros((4, 50), dtype=torch.int8, device="cuda"),
+              torch.zeros((4, 131072), dtype=torch.int8, device="cuda")):
+        with pytest.raises(ValueError):
+            vq.Int8Layer(w, ws)
+    vq.Int8Layer(base.new_zeros((4, 0)), ws)                     # without inputs nothing is read
+    vq.Int8Layer(base.new_zeros((1, 50)), ws[:1])                # one row has no stride
