@@ -65,22 +65,18 @@ cudaError_t set_func_attr(const void* func, cudaFuncAttribute attr, int value) {
   static std::vector<Entry> done;
   int dev = 0;
   cudaGetDevice(&dev);
-  {
-    std::lock_guard<std::mutex> lock(mu);
-    for (const Entry& e : done)
-      if (e.dev == dev && e.func == func && e.attr == attr &&
-          (e.value == value || (attr == cudaFuncAttributeMaxDynamicSharedMemorySize && e.value >= value)))
-        return cudaSuccess;
-  }
+  // The lock spans looking up and setting: between the two, another thread
+  // could set a larger size that this one's would then take back.
+  std::lock_guard<std::mutex> lock(mu);
+  Entry* at = nullptr;
+  for (Entry& e : done)
+    if (e.dev == dev && e.func == func && e.attr == attr) at = &e;
+  if (at && (at->value == value || (attr == cudaFuncAttributeMaxDynamicSharedMemorySize && at->value >= value)))
+    return cudaSuccess;
   const cudaError_t err = cudaFuncSetAttribute(func, attr, value);
   if (err != cudaSuccess) return err;
-  std::lock_guard<std::mutex> lock(mu);
-  for (Entry& e : done)
-    if (e.dev == dev && e.func == func && e.attr == attr) {
-      if (attr != cudaFuncAttributeMaxDynamicSharedMemorySize || value > e.value) e.value = value;
-      return cudaSuccess;
-    }
-  done.push_back({dev, func, attr, value});
+  if (at) at->value = value;
+  else done.push_back({dev, func, attr, value});
   return cudaSuccess;
 }
 int device_smem_optin() { return attrs_for_current_device().smem_optin; }
