@@ -148,8 +148,14 @@ __global__ void __launch_bounds__(kPrepThreads) experts_prep_kernel(
 // book costs 1024 gathers at the 0.84 a clock that L2 hands out, 1220 clocks.
 // Measured (B200, 148 SMs, weights cold): two 14336 x 4096 experts of 12 + 8 bits
 // for one row 53 us (0.35 us a step, 20 us before the first and after the last);
-// eight of them for 8192 rows 1.02 ms, 943 TFLOP/s (1.2 ms under the power cap);
-// sixteen 4096 x 2048 experts with 2^16 books for 62 rows each 99 us.
+// eight of them for 8192 rows, 1024 each, 1.02 ms a call, 942 TFLOP/s, and 1.17 ms
+// (821) in a loop of calls under the power cap; sixteen 4096 x 2048 experts with
+// 2^16 books for 62 rows each 99 us.
+//
+// W's two centroids are added in fp16, since the tensor cores take 16-bit
+// operands and a product of its own for each book would double their work: half
+// a step of 2^-11 per weight, 2.1e-4 of y in the root mean square (one book: no
+// rounding, 6e-7).
 //
 //  * Sixteen producer warps decode W.  They work in four groups of 128 threads,
 //    group i taking every fourth step (64 columns) from the i-th on; a thread
@@ -264,7 +270,8 @@ struct Line {
 
 // Cost of a step of a tile of n rows: a part that does not depend on n (W is
 // decoded) and one that does.  Measured (ns): 500 + 1.5 n with books in shared
-// memory, 700 + 2.1 n with a 2^16 book, about the same proportion.
+// memory, 700 + 2.1 n with a 2^16 book, about the same proportion; 1670 + 2.0 n in
+// the general kernel (10 + 6 bits, tiled), for which this counts rows too high.
 __host__ __device__ constexpr int step_cost(int n) { return 330 + n; }
 
 // Rows of a token tile of an expert with `count` rows in `tt` tiles.
@@ -506,7 +513,12 @@ __host__ __device__ constexpr int acc_rows(bool in_tmem) { return in_tmem ? 192 
 
 // B1 > 0: d <= 8, books of 2^B1 and 2^B2 (0: no second) entries; the second
 // staged, the first staged or (B1 = 16) read through L2 with d = 8.  B1 = 0:
-// any layer.
+// any layer, field by field.  Measured (eight 4096 x 4096 experts, cold, ps a
+// vector in row order / tiled), 16 rows each: 12 + 8 bits 5.2 / 3.8, 16 bits 5.1 /
+// 4.9; B1 = 0: 10 + 6 bits 13.7 / 11.2, 11 bits 7.8, 16 bits of d = 6 11.6 / 10.9, d
+// = 16 13 to 15 for twice the values.  256 rows each: 12 + 8 bits 8.3 / 7.3, 10 + 6
+// bits 18 / 14, but 12 + 12 and 13 + 13 bits 62 and 84: 128 KB of staged books leave
+// room for token tiles of 64 and 32 rows, and W is decoded for each.
 template <int LAYOUT, int B1, int B2>
 __global__ void __launch_bounds__(kThreads, 1)
     gemm_experts_kernel(const __grid_constant__ Maps maps,

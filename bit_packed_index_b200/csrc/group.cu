@@ -219,8 +219,8 @@ __device__ __forceinline__ float load1(const void* p, int64_t i) {
 
 constexpr int kCombineThreads = 256;
 // Picks whose loads are in flight together, and blocks per SM.  8192 tokens x 8
-// picks x 4096 columns: 8 and 2 took 124 us, 8 and 4 110, 4 and 6 123, 4 and 5
-// 99 us (6.1 TB/s); 2048 x 2 x 8192: 49, 40, 33, 24 us.
+// picks x 4096 columns (cold): 8 and 2 took 124 us, 8 and 4 108, 4 and 6 142, 4
+// and 4 103, 4 and 5 102 us (5.9 TB/s); 2048 x 2 x 8192: 52, 40, 44, 31, 29 us.
 constexpr int kCombineAhead = 4;
 constexpr int kCombineBlocks = 5;
 
@@ -308,7 +308,7 @@ cudaError_t launch_combine(bool vec, const void* z, int z_rows, int n, int64_t l
 }
 
 // Whether a cluster of sixteen CTAs with this much shared memory fits the
-// current device (remembered per device for the largest size asked).
+// current device (remembered per device and size).
 bool wide_clusters(size_t smem) {
   struct Entry {
     int dev;

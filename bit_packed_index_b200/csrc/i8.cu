@@ -7,7 +7,10 @@
 // 2^-22 < 4e-5, so the nearest integer is right unless the product lies within
 // 1e-4 of a half.  There the sign of x - (n + 1/2) s decides, which one fused
 // multiply-add gives exactly (its only rounding cannot change a sign).  One
-// element in 5000 takes that path; the kernel stays at the memory's speed.
+// element in 5000 takes that path.  Measured (B200, cold): 4096 x 8192 from bf16
+// 33 us (3.0 TB/s, less than half of what memory gives: a row's two passes and
+// two barriers leave little in flight); rows that do not start on 16 bytes are
+// read value by value, 4096 x 8190 90 us (1.1 TB/s).
 #include <algorithm>
 #include <cstdlib>
 #include <type_traits>
@@ -170,10 +173,10 @@ cudaError_t launch_quant(const uint16_t* x, int rows, int n, int64_t ldx, int8_t
 // swizzled rows (128 values of k a step); rows and columns past the matrices
 // read as zeros.  A thread of the epilogue owns one output channel, so its
 // scale and bias are registers and a warp stores 32 neighbouring outputs of a
-// token at a time.  Measured (B200): 24 x 8192 x 8192 16.3 us (4.1 TB/s of
-// weights, cold), 16 x 16384 x 16384 47 us (5.7 TB/s), 4096 x 8192 x 8192 167 us
-// (3.3 POP/s; tensor pipe 86 % busy at 2048 rows), about 200 us once the power
-// cap holds the clocks down.
+// token at a time.  Measured (B200, the product alone): 24 x 8192 x 8192 16.6 us
+// (4.0 TB/s of weights, cold), 16 x 16384 x 16384 46 us (5.8 TB/s), 4096 x 8192 x
+// 8192 159 to 167 us for a few calls (3.3 to 3.5 POP/s; tensor pipe 86 % busy at
+// 2048 rows), 194 us (2.8 POP/s) once the power cap holds the clocks down.
 // ---------------------------------------------------------------------------
 using namespace sm100;
 
@@ -249,8 +252,8 @@ __device__ __forceinline__ void store_rows(vq_dtype yt, uint8_t* yo, int64_t ldb
 
 // ---- few rows: W's bytes are the bound ------------------------------------
 // A cluster of S CTAs shares a tile of 128 outputs, each CTA a run of k, so
-// that even a layer of 1024 outputs keeps most SMs loading.  The partial sums
-// meet in distributed shared memory: integers, so the split changes nothing
+// that a layer of few outputs keeps up to eight times as many SMs loading (64 of
+// 148 for 1024 outputs).  The partial sums meet in distributed shared memory: integers, so the split changes nothing
 // in y, and no workspace, counter or second launch is needed.
 struct NarrowCtrl {
   uint64_t full[kMaxStages], empty[kMaxStages], acc;
@@ -647,10 +650,10 @@ long long wait_budget() {
 
 // Splits of the narrow kernel (a power of two): double the cluster while the
 // grid stays within two CTAs per SM and each CTA keeps at least four steps (512
-// bytes of k).  24 x 8192 x 8192 with 2, 4 (chosen) and 8 CTAs a cluster: 18.0,
-// 16.4, 19.8 us.  It doubles once too often where the cluster's barriers cost
-// more than the loads gain: 4 x 4096 x 4096 with 4 and 8 (chosen) 5.3, 5.8; 16 x
-// 14336 x 4096 with 1 and 2 (chosen) 14.1, 15.6.
+// bytes of k).  Cold weights, 1, 2, 4, 8 CTAs a cluster, the choice marked: 1 x
+// 1024 x 16384 25.7, 15.6, 10.4, 8.3* us; 4 x 4096 x 4096 9.2, 8.2, 7.0, 6.9*; 24 x
+// 8192 x 8192 18.1, 17.4, 16.3*, 19.0; 16 x 14336 x 4096 13.2, 15.1*, -, 23.2, where
+// 112 tiles fill the SMs already and the rule doubles once too often.
 int narrow_splits(int tiles, int num_kt, int sms) {
   int s = 1;
   while (s < 8 && tiles * s * 2 <= 2 * sms && num_kt >= 8 * s) s *= 2;
